@@ -24,6 +24,7 @@ QMOE_OK = 0
 QMOE_F32 = 0
 QMOE_BF16 = 1
 QMOE_F32_DIGITS = 2      # f32 x, activations rounded to 18-bit block fixed point
+QMOE_MXFP4 = 3           # MXFP4 rows (qmoe_mx_* products)
 STATUS = {0: "QMOE_OK", 1: "QMOE_ERR_NULL", 2: "QMOE_ERR_SHAPE", 3: "QMOE_ERR_ALIGN",
           4: "QMOE_ERR_UNSUPPORTED", 5: "QMOE_ERR_WORKSPACE", 6: "QMOE_ERR_ALIAS",
           7: "QMOE_ERR_ABI", 8: "QMOE_ERR_HIP", 9: "QMOE_ERR_SCRATCH"}
@@ -56,6 +57,18 @@ class qmoe_layer_ws_view(ctypes.Structure):
                 ("inv", ctypes.c_int64), ("n_invalid", ctypes.c_int64)]
 
 
+class qmoe_mxmat(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("q", ctypes.c_void_p), ("s", ctypes.c_void_p),
+                ("q_expert_stride", ctypes.c_int64), ("s_expert_stride", ctypes.c_int64)]
+
+
+class qmoe_mx_layer_desc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("experts", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("gate", qmoe_mxmat),
+                ("up", qmoe_mxmat), ("down", qmoe_mxmat)]
+
+
 EXPORTS = ["qmoe_abi_version", "qmoe_status_str", "qmoe_packed_bytes", "qmoe_scale_count",
            "qmoe_pack", "qmoe_unpack", "qmoe_matvec_workspace_bytes", "qmoe_matvec",
            "qmoe_expert_ffn_workspace_bytes", "qmoe_expert_ffn",
@@ -65,7 +78,9 @@ EXPORTS = ["qmoe_abi_version", "qmoe_status_str", "qmoe_packed_bytes", "qmoe_sca
            "qmoe_cache_prepare", "qmoe_cache_resident", "qmoe_cache_device_state_bytes",
            "qmoe_cache_device_init", "qmoe_cache_prepare_device", "qmoe_layer_logits_workspace_bytes",
            "qmoe_layer_logits", "qmoe_layer_noalloc", "qmoe_prefill_pass_rows",
-           "qmoe_stream_probe"]
+           "qmoe_stream_probe", "qmoe_mx_code_bytes", "qmoe_mx_scale_bytes", "qmoe_mx_quantize",
+           "qmoe_mx_dequantize", "qmoe_mx_workspace_bytes", "qmoe_mx_matmul", "qmoe_mx_grouped",
+           "qmoe_mx_layer_workspace_bytes", "qmoe_mx_layer"]
 
 _lib = None
 
@@ -122,6 +137,18 @@ def load(path: str | None = None):
                                               vp, i32, vp, vp]),
         "qmoe_prefill_pass_rows": (i32, []),
         "qmoe_stream_probe": (ctypes.c_int, [vp, i64, i32, vp, vp]),
+        "qmoe_mx_code_bytes": (sz, [i64, i64]),
+        "qmoe_mx_scale_bytes": (sz, [i64, i64]),
+        "qmoe_mx_quantize": (ctypes.c_int, [vp, i32, i64, i64, i64, vp, vp, vp]),
+        "qmoe_mx_dequantize": (ctypes.c_int, [vp, vp, i64, i64, vp, i32, i64, vp]),
+        "qmoe_mx_workspace_bytes": (sz, [ctypes.POINTER(qmoe_mxmat), i32, i32, i64]),
+        "qmoe_mx_matmul": (ctypes.c_int, [ctypes.POINTER(qmoe_mxmat), i32, vp, vp, i32, i64, i32,
+                                          vp, i64, vp, sz, vp]),
+        "qmoe_mx_grouped": (ctypes.c_int, [ctypes.POINTER(qmoe_mxmat), i32, i32, vp, vp, i32, i64,
+                                           vp, vp, i32, i32, i32, vp, i64, vp, sz, vp]),
+        "qmoe_mx_layer_workspace_bytes": (sz, [ctypes.POINTER(qmoe_mx_layer_desc), i32, i32, i32]),
+        "qmoe_mx_layer": (ctypes.c_int, [ctypes.POINTER(qmoe_mx_layer_desc), i32, vp, i32, vp, vp,
+                                         i32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -569,3 +596,234 @@ def layer_worklist_from_ws(layer: QLayer, ws, tokens, k, x_dtype):
     E = layer.experts
     return dict(counts=i32(v.counts, E), offsets=i32(v.offsets, E + 1), pairs=i32(v.pairs, n),
                 inv=i32(v.inv, n), n_invalid=i32(v.n_invalid, 1))
+
+
+# ------------------------------------------------------------------ MXFP4 ---
+
+_MX_TYPES = {torch.float32: QMOE_F32, torch.bfloat16: QMOE_BF16}
+
+
+def _rows(t, name):
+    """Pointer, row count and elements between rows of a device tensor whose
+    last dimension is dense (1-D: one row)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in _MX_TYPES:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() == 1:
+        t = t[None]
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, cols] with dense rows")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ctypes.c_void_p(t.data_ptr()), t.shape[0], max(ld, t.shape[1])
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the weights or first operand on {device}")
+
+
+def qmoe_mx_quantize(x, q=None, s=None, stream=None):
+    """f32 or bf16 rows [rows, cols] (rows may be strided) -> MXFP4 codes
+    uint8 [rows, ceil(cols/32) * 16] and scale bytes uint8 [rows, ceil(cols/32)]."""
+    p, rows, ld = _rows(x, "x")
+    cols = x.shape[-1]
+    nb = (cols + 31) // 32
+    q = torch.empty(rows, nb * 16, dtype=torch.uint8, device=x.device) if q is None else q
+    s = torch.empty(rows, nb, dtype=torch.uint8, device=x.device) if s is None else s
+    _mx_pair(q, s, rows, cols, "q", "s")
+    _same_device(x.device, q=q, s=s)
+    with _on(x.device):
+        _check(load().qmoe_mx_quantize(p, _MX_TYPES[x.dtype], rows, cols, ld, _ptr(q), _ptr(s),
+                                       _stream(stream)), "qmoe_mx_quantize")
+    return q, s
+
+
+def qmoe_mx_dequantize(q, s, cols, dtype=torch.float32, out=None, stream=None):
+    """MXFP4 rows -> f32 or bf16 values [rows, cols]; `out` rows may be strided."""
+    rows = q.shape[0]
+    _mx_pair(q, s, rows, cols, "q", "s")
+    if out is None:
+        if dtype not in _MX_TYPES:
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+        out = torch.empty(rows, cols, dtype=dtype, device=q.device)
+    p, r, ld = _rows(out, "out")
+    if r != rows or out.shape[-1] != cols:
+        raise ValueError(f"out must be [{rows}, {cols}]")
+    _same_device(q.device, s=s, out=out)
+    with _on(q.device):
+        _check(load().qmoe_mx_dequantize(_ptr(q), _ptr(s), rows, cols, p, _MX_TYPES[out.dtype], ld,
+                                         _stream(stream)), "qmoe_mx_dequantize")
+    return out
+
+
+class _on:
+    """The device a call runs on, made current for its length where it is not
+    (launches and `current_stream` go by the current device)."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _mx_pair(q, s, rows, cols, nq, ns):
+    """Codes [rows, nb * 16] and scales [rows, nb] of MXFP4 rows."""
+    nb = (cols + 31) // 32
+    _dev(q, nq, torch.uint8)
+    _dev(s, ns, torch.uint8)
+    if tuple(q.shape) != (rows, nb * 16) or tuple(s.shape) != (rows, nb):
+        raise ValueError(f"{nq}, {ns} must be [{rows}, {nb * 16}] and [{rows}, {nb}] for {cols} columns, "
+                         f"got {tuple(q.shape)} and {tuple(s.shape)}")
+
+
+class MxMat:
+    """An MXFP4 matrix: codes q [rows, nb * 16] and scales s [rows, nb], nb =
+    ceil(cols / 32), as qmoe_mx_quantize writes them; or a stack [E, ...]."""
+
+    def __init__(self, q, s, cols):
+        _dev(q, "q", torch.uint8)
+        _dev(s, "s", torch.uint8)
+        nb = (cols + 31) // 32
+        if q.dim() not in (2, 3) or q.shape[-1] != nb * 16 or tuple(s.shape) != (*q.shape[:-1], nb):
+            raise ValueError(f"q, s must be [E?, rows, {nb * 16}] and [E?, rows, {nb}] for {cols} columns, "
+                             f"got {tuple(q.shape)} and {tuple(s.shape)}")
+        _same_device(q.device, s=s)
+        self.q, self.s, self.cols, self.rows = q, s, cols, q.shape[-2]
+        self.experts = q.shape[0] if q.dim() == 3 else 1
+        self.device = q.device
+        m = qmoe_mxmat()
+        m.struct_size = ctypes.sizeof(qmoe_mxmat)
+        m.rows, m.cols, m.q, m.s = self.rows, cols, q.data_ptr(), s.data_ptr()
+        m.q_expert_stride = q.stride(0) if q.dim() == 3 else 0
+        m.s_expert_stride = s.stride(0) if s.dim() == 3 else 0
+        self.desc = m
+        self.ref = ctypes.byref(m)
+
+
+class MxLayer:
+    """The MXFP4 weights of one MoE layer: stacks gate and up [E, inter,
+    hidden] and down [E, hidden, inter]."""
+
+    def __init__(self, gate: MxMat, up: MxMat, down: MxMat):
+        self.gate, self.up, self.down = gate, up, down
+        self.experts, self.hidden, self.inter = gate.experts, gate.cols, gate.rows
+        self.device = gate.device
+        for m, n, shape in ((up, "up", (self.experts, self.inter, self.hidden)),
+                            (down, "down", (self.experts, self.hidden, self.inter))):
+            if (m.experts, m.rows, m.cols) != shape:
+                raise ValueError(f"{n} must be {shape}, got {(m.experts, m.rows, m.cols)}")
+            _same_device(self.device, **{n: m.q})
+        d = qmoe_mx_layer_desc()
+        d.struct_size = ctypes.sizeof(qmoe_mx_layer_desc)
+        d.experts, d.hidden, d.inter = self.experts, self.hidden, self.inter
+        d.gate, d.up, d.down = gate.desc, up.desc, down.desc
+        self.desc = d
+        self.ref = ctypes.byref(d)
+
+    def workspace_bytes(self, tokens, k, x_dtype):
+        return int(load().qmoe_mx_layer_workspace_bytes(self.ref, tokens, k, x_dtype))
+
+
+def _mx_operand(W, x, x_s):
+    """(type code, pointer of x, of x_s, rows, elements between rows)."""
+    if x_s is not None:
+        _mx_pair(x, x_s, x.shape[0], W.cols, "x", "x_s")
+        _same_device(W.device, x=x, x_s=x_s)
+        return QMOE_MXFP4, _ptr(x), _ptr(x_s), x.shape[0], W.cols
+    p, rows, ld = _rows(x, "x")
+    if x.shape[-1] != W.cols:
+        raise ValueError(f"x has {x.shape[-1]} columns, the matrix {W.cols}")
+    _same_device(W.device, x=x)
+    return _MX_TYPES[x.dtype], p, None, rows, ld
+
+
+def _mx_out(W, x, x_s, n, out, out_dtype):
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.float32 if x_s is not None else x.dtype
+        if out_dtype not in _MX_TYPES:
+            raise TypeError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+        out = torch.empty(n, W.rows, dtype=out_dtype, device=W.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    p, rows, ld = _rows(out, "out")
+    if rows != n or out.shape[-1] != W.rows:
+        raise ValueError(f"out must be [{n}, {W.rows}]")
+    _same_device(W.device, out=out)
+    return out, p, ld
+
+
+def qmoe_mx_matmul(W: MxMat, x, x_s=None, out=None, out_dtype=None, ws=None, stream=None):
+    """y = x W^T for one MXFP4 matrix.  x f32 or bf16 [batch, cols] (rows may be
+    strided), or MXFP4 codes with x_s their scales.  y has out_dtype (default:
+    x's type, f32 for MXFP4 rows)."""
+    code, p, ps, rows, ld = _mx_operand(W, x, x_s)
+    y, py, y_ld = _mx_out(W, x, x_s, rows, out, out_dtype)
+    lib = load()
+    with _on(W.device):
+        nb = lib.qmoe_mx_workspace_bytes(W.ref, code, rows, ld)
+        ws = _workspace(nb, W.device, ws, stream) if nb else None
+        _check(lib.qmoe_mx_matmul(W.ref, code, p, ps, rows, ld, _MX_TYPES[y.dtype], py, y_ld,
+                                  _ptr(ws), nb, _stream(stream)), "qmoe_mx_matmul")
+    return y
+
+
+def qmoe_mx_grouped(W: MxMat, x, offsets, pairs=None, k=1, x_s=None, out=None, out_dtype=None,
+                    ws=None, stream=None):
+    """y[r] = W_e x[pairs[r] // k] (x[r] without pairs) for the rows offsets[e]
+    <= r < offsets[e + 1] of each expert e; offsets int32 [E + 1] and pairs
+    int32 [n] as qmoe_worklist returns them.  Rows no expert holds are not
+    written."""
+    _dev(offsets, "offsets", torch.int32)
+    if offsets.numel() != W.experts + 1:
+        raise ValueError(f"offsets must hold {W.experts + 1} values, got {offsets.numel()}")
+    code, p, ps, rows, ld = _mx_operand(W, x, x_s)
+    n = rows
+    if pairs is not None:
+        _dev(pairs, "pairs", torch.int32)
+        n = pairs.numel()
+    _same_device(W.device, offsets=offsets, pairs=pairs)
+    y, py, y_ld = _mx_out(W, x, x_s, n, out, out_dtype)
+    lib = load()
+    with _on(W.device):
+        nb = lib.qmoe_mx_workspace_bytes(W.ref, code, rows, ld)
+        ws = _workspace(nb, W.device, ws, stream) if nb else None
+        _check(lib.qmoe_mx_grouped(W.ref, W.experts, code, p, ps, rows, ld, _ptr(offsets),
+                                   _ptr(pairs), k, n, _MX_TYPES[y.dtype], py, y_ld, _ptr(ws), nb,
+                                   _stream(stream)), "qmoe_mx_grouped")
+    return y
+
+
+def qmoe_mx_layer(layer: MxLayer, x, topk_ids, topk_w, out=None, ws=None, stream=None):
+    """Routed MoE layer with MXFP4 experts: out[t] = sum_j w[t,j] *
+    ffn_{ids[t,j]}(x_t), in x's type (f32 or bf16)."""
+    _dev(x, "x")
+    _dev(topk_ids, "topk_ids", torch.int32)
+    _dev(topk_w, "topk_w", torch.float32)
+    code = _dtype_code(x)
+    T, k = topk_ids.shape
+    if tuple(x.shape) != (T, layer.hidden) or topk_w.shape != topk_ids.shape:
+        raise ValueError(f"x must be [{T}, {layer.hidden}] and topk_w [{T}, {k}], got "
+                         f"{tuple(x.shape)} and {tuple(topk_w.shape)}")
+    if out is None:
+        out = torch.empty_like(x)
+    elif _dev(out, "out", x.dtype).shape != x.shape:
+        raise ValueError(f"out must be {tuple(x.shape)}")
+    _same_device(layer.device, x=x, topk_ids=topk_ids, topk_w=topk_w, out=out)
+    lib = load()
+    with _on(layer.device):
+        nb = lib.qmoe_mx_layer_workspace_bytes(layer.ref, T, k, code)
+        ws = _workspace(nb, layer.device, ws, stream)
+        _check(lib.qmoe_mx_layer(layer.ref, code, _ptr(x), T, _ptr(topk_ids), _ptr(topk_w), k,
+                                 _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "qmoe_mx_layer")
+    return out

@@ -1,0 +1,210 @@
+// MXFP4 (microscaled 4-bit floats): operand descriptions and device helpers
+// shared by the mx_*.hip kernels.
+//
+// Format.  A row of K values is ceil(K / 32) blocks; a block is 16 bytes of
+// codes (element 2j in the low nibble of byte j) and one scale byte c that
+// stands for 2^(c - 127), c = 255 for NaN.  A code is sign, 2 exponent bits
+// and 1 mantissa bit: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+#pragma once
+
+#include "common.h"
+
+namespace qmoe {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int MX_BLOCK = 32;
+
+__host__ __device__ inline int mx_blocks(int64_t cols) { return (int)((cols + MX_BLOCK - 1) / MX_BLOCK); }
+
+// A stack of MXFP4 matrices: codes [rows][nb][16], scales [rows][nb].
+struct MxMat {
+    const uint8_t *q, *s;
+    int64_t q_stride, s_stride;   // bytes between experts
+    int rows, nb;
+};
+
+// Rows of the other operand.  bf16 parts: `parts` (1, or 3 that sum to an f32
+// value exactly) rows of `width` bf16 behind each other, width a multiple of
+// 128, zero past the row's own columns; ld = bytes per row of all parts.
+// MXFP4: ld = nb * 16 bytes of codes, scales in s with nb bytes per row.
+struct MxX {
+    const uint8_t *v;
+    const uint8_t *s;
+    int64_t ld;
+    int64_t rows;
+    int width;
+};
+
+// Row groups.  offsets == nullptr: one group of n rows (matrix 0).  Else rows
+// offsets[e] .. offsets[e + 1] of the output belong to matrix e; row r reads
+// x row pairs[r] / k, or r itself without pairs.
+struct MxGroups {
+    const int32_t *offsets;
+    const int32_t *pairs;
+    int k, experts, n;
+};
+
+// What a product writes.
+enum { MX_OUT_F32 = 0, MX_OUT_BF16 = 1 };
+struct MxOut {
+    void *y;            // rows of y (f32 or bf16), or the parts of h
+    int64_t ld;         // elements between rows of y; bytes between rows of h
+    int type;           // MX_OUT_*
+    const float *w;     // row r is multiplied by w[wpairs[r]] (nullptr: no weights)
+    const int32_t *wpairs;
+    int width;          // h: padded width of a part
+    int vec;            // four consecutive outputs of a row may be stored at once
+};
+
+__device__ __forceinline__ float mx_scale(uint32_t c) {
+    uint32_t b = c << 23;
+    b = c == 0 ? 0x00400000u : b;      // 2^-127 is subnormal
+    b = c == 255 ? 0x7fc00000u : b;
+    return __uint_as_float(b);
+}
+
+// Eight codes (a dword) times a power of two as bf16, exact: a code has two
+// significant bits and bf16 the exponent range of the scales (results below
+// 2^-126 are subnormal and kept).
+__device__ __forceinline__ u32x4 mx_decode8(uint32_t d, float scale) {
+    union { bf16x2 p[4]; u32x4 v; } r;
+    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
+    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
+    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
+    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
+    return r.v;
+}
+
+// f32 as three bf16 parts, exact: each part takes the top 8 significant bits
+// that are left (truncation), 3 x 8 = 24.  A NaN or infinity goes into the
+// first part alone (inf - inf would make a NaN of it).  Bits below 2^-133
+// (bf16's smallest subnormal) are lost.
+__device__ __forceinline__ void mx_split3(float x, uint16_t p[3]) {
+    const uint32_t b = __float_as_uint(x);
+    const bool fin = (b & 0x7f800000u) != 0x7f800000u;
+    // a NaN whose bits all lie in the lower half stays a NaN
+    const uint32_t top = (b & 0xffff0000u) | (!fin && (b & 0x007fffffu) ? 0x00400000u : 0u);
+    const float r1 = fin ? x - __uint_as_float(top) : 0.0f;
+    const uint32_t m = __float_as_uint(r1) & 0xffff0000u;
+    const float r2 = r1 - __uint_as_float(m);
+    p[0] = (uint16_t)(top >> 16);
+    p[1] = (uint16_t)(m >> 16);
+    p[2] = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
+__device__ __forceinline__ uint16_t mx_bf16(float x) {
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+struct MxTile {
+    int e, pos0, rows, cb;
+};
+
+// The work item of this block: a tile of at most BM rows of one group and a
+// column block.  Every wave of the block runs it (no LDS): lane l sums the
+// tiles of its share of the experts, a scan over the wave finds the lane the
+// tile falls to, and that lane walks its experts.  Offsets are clamped to
+// [0, n], so no value of theirs leads outside the output.  The GPU hands
+// linear block ids to its 8 XCDs round-robin and each XCD has an L2 of its
+// own; each is given one contiguous run of the items, the column blocks of a
+// tile side by side.
+__device__ __forceinline__ bool mx_find(const MxGroups &g, int bm, int ncb, MxTile &t) {
+    const int lane = lane_id();
+    int total, mine = 0, before = 0, per = 0;
+    if (!g.offsets) {
+        total = (g.n + bm - 1) / bm;
+    } else {
+        per = (g.experts + QMOE_WAVE - 1) / QMOE_WAVE;
+        int last = 0;
+        for (int i = 0; i <= per; i++) {
+            const int e = min(lane * per + i, g.experts);
+            const int o = min(max(g.offsets[e], 0), g.n);
+            if (i > 0) mine += (max(o - last, 0) + bm - 1) / bm;
+            last = o;
+        }
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < QMOE_WAVE; o <<= 1) {
+            const int y = __shfl_up(inc, o, QMOE_WAVE);
+            if (lane >= o) inc += y;
+        }
+        before = inc - mine;
+        total = __builtin_amdgcn_readlane(inc, QMOE_WAVE - 1);
+    }
+    const int64_t items = (int64_t)total * ncb;
+    const int64_t per_xcd = (items + 7) / 8;
+    const int64_t w = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per_xcd || w >= items) return false;
+    const int tile = __builtin_amdgcn_readfirstlane((int)(w / ncb));
+    t.cb = __builtin_amdgcn_readfirstlane((int)(w - (int64_t)tile * ncb));
+    if (!g.offsets) {
+        t.e = 0;
+        t.pos0 = tile * bm;
+        t.rows = min(bm, g.n - t.pos0);
+        return true;
+    }
+    const bool here = tile >= before && tile < before + mine;
+    int e = 0, pos0 = 0, rows = 0;
+    if (here) {
+        int left = tile - before;
+        int last = min(max(g.offsets[min(lane * per, g.experts)], 0), g.n);
+        for (int i = 1; i <= per; i++) {
+            const int x = min(lane * per + i, g.experts);
+            const int o = min(max(g.offsets[x], 0), g.n);
+            const int c = max(o - last, 0);
+            const int nt = (c + bm - 1) / bm;
+            if (left >= 0 && left < nt) {
+                e = x - 1;
+                pos0 = last + left * bm;
+                rows = min(bm, c - left * bm);
+            }
+            left -= nt;
+            last = o;
+        }
+    }
+    const int src = __ffsll((unsigned long long)__ballot(here)) - 1;
+    t.e = __builtin_amdgcn_readlane(e, src);
+    t.pos0 = __builtin_amdgcn_readlane(pos0, src);
+    t.rows = __builtin_amdgcn_readlane(rows, src);
+    return true;
+}
+
+// x row of output row `pos`; -1 where its pair names no row of x.
+__device__ __forceinline__ int64_t mx_source(const MxGroups &g, const MxX &x, int pos) {
+    if (!g.pairs) return pos;
+    const int p = g.pairs[pos];
+    const int r = p / g.k;
+    return p < 0 || r >= x.rows ? -1 : r;
+}
+
+inline unsigned mx_grid(int64_t items) { return (unsigned)(((items + 7) / 8) * 8); }
+// Upper bound of the tiles of bm rows that n rows in `experts` groups make.
+inline int64_t mx_max_tiles(const MxGroups &g, int bm) {
+    const int64_t t = (g.n + (int64_t)bm - 1) / bm;
+    return g.offsets ? t + (g.n < g.experts ? g.n : g.experts) : t;
+}
+
+// ---- launchers (host side; shapes are validated by the C ABI layer) -------
+
+hipError_t launch_mx_quantize(const void *x, bool f32, int64_t rows, int cols, int64_t ld,
+                              uint8_t *q, uint8_t *s, hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int cols, void *y,
+                                bool f32, int64_t ld, hipStream_t st);
+// x [rows][cols] -> bf16 parts (3 for f32, 1 for bf16) of `width` columns.
+hipError_t launch_mx_parts(const void *x, bool f32, int64_t rows, int cols, int64_t ld,
+                           uint16_t *parts, int width, hipStream_t st);
+// Products.  parts: 0 (x is MXFP4), 1 or 3.  up.q != nullptr: h parts of
+// silu(W x) * (up x) instead of y (out.y, out.ld, out.width).
+hipError_t launch_mx_stream(const MxMat &w, const MxMat &up, const MxX &x, int parts,
+                            const MxGroups &g, const MxOut &out, hipStream_t st);
+hipError_t launch_mx_tile(const MxMat &w, const MxMat &up, const MxX &x, int parts,
+                          const MxGroups &g, const MxOut &out, hipStream_t st);
+hipError_t launch_mx_tile_fp4(const MxMat &w, const MxX &x, const MxGroups &g, const MxOut &out,
+                              hipStream_t st);
+// out[t] = sum_j y[inv[t * k + j]] in pick order (f32 sums), as f32 or bf16.
+hipError_t launch_mx_combine(const float *y, const int32_t *inv, int tokens, int k, int cols,
+                             void *out, bool f32, hipStream_t st);
+
+}  // namespace qmoe

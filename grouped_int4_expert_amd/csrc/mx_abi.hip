@@ -1,0 +1,364 @@
+// C ABI of the MXFP4 entry points: checks, workspace layout and launch
+// sequencing.  As in abi.hip every check runs before the first HIP call.
+#include "abi_util.h"
+#include "launch.h"
+#include "mx.h"
+
+using namespace qmoe;
+
+namespace {
+
+constexpr int64_t LIM31 = (int64_t)1 << 31;
+
+// The kernels address one matrix through buffer descriptors whose lanes past
+// a row's end use an offset of 2^31.
+int check_mxmat(const qmoe_mxmat *m, int experts) {
+    if (!m) return QMOE_ERR_NULL;
+    if (m->struct_size != sizeof(qmoe_mxmat)) return QMOE_ERR_ABI;
+    if (m->rows <= 0 || m->cols <= 0 || experts < 1 || experts > MAX_EXPERTS) return QMOE_ERR_SHAPE;
+    const int64_t nb = mx_blocks(m->cols), qb = m->rows * nb * 16, sb = m->rows * nb;
+    if (qb >= LIM31) return QMOE_ERR_UNSUPPORTED;
+    if (!m->q || !m->s) return QMOE_ERR_NULL;
+    if (!aligned16(m->q) || !aligned16(m->s)) return QMOE_ERR_ALIGN;
+    if (experts > 1) {
+        if (m->q_expert_stride < qb || m->s_expert_stride < sb) return QMOE_ERR_SHAPE;
+        if (m->q_expert_stride % 16 != 0) return QMOE_ERR_ALIGN;
+        // 2^50: no stack is larger, and the sizes below stay within 64 bits
+        if (m->q_expert_stride >> 40 || m->s_expert_stride >> 40) return QMOE_ERR_SHAPE;
+    }
+    return QMOE_OK;
+}
+
+// Bytes from the first to the last one a stack of `experts` matrices uses.
+int64_t span_q(const qmoe_mxmat *m, int experts) {
+    return (experts - 1) * m->q_expert_stride + (int64_t)m->rows * mx_blocks(m->cols) * 16;
+}
+int64_t span_s(const qmoe_mxmat *m, int experts) {
+    return (experts - 1) * m->s_expert_stride + (int64_t)m->rows * mx_blocks(m->cols);
+}
+bool overlaps_mat(const void *p, int64_t n, const qmoe_mxmat *m, int experts) {
+    return overlap(p, n, m->q, span_q(m, experts)) || overlap(p, n, m->s, span_s(m, experts));
+}
+
+MxMat to_mx(const qmoe_mxmat *m) {
+    return MxMat{m->q, m->s, m->q_expert_stride, m->s_expert_stride, m->rows, mx_blocks(m->cols)};
+}
+
+int pad128(int64_t cols) { return (int)((cols + 127) / 128 * 128); }
+int parts_of(int dtype) { return dtype == QMOE_F32 ? 3 : 1; }
+int elem_bytes(int dtype) { return dtype == QMOE_F32 ? 4 : 2; }
+bool float_type(int dtype) { return dtype == QMOE_F32 || dtype == QMOE_BF16; }
+
+// bf16 rows of whole 128-input steps that start at 16-byte boundaries are the
+// products' operand as they are; any other f32 or bf16 rows are first turned
+// into parts in the workspace.
+bool direct_rows(int dtype, int64_t cols, int64_t ld) {
+    return dtype == QMOE_BF16 && cols % 128 == 0 && ld % 8 == 0;
+}
+int64_t parts_bytes(int dtype, int64_t rows, int64_t cols, int64_t ld) {
+    if (dtype == QMOE_MXFP4 || direct_rows(dtype, cols, ld)) return 0;
+    return align256(rows * parts_of(dtype) * pad128(cols) * 2);
+}
+
+// Bytes a strided [rows][cols] array spans.
+int64_t span(int64_t rows, int64_t cols, int64_t ld, int bytes) {
+    return rows > 0 ? ((rows - 1) * ld + cols) * bytes : 0;
+}
+
+// The operand x of a product, with its parts written first where it needs
+// them.
+hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, int cols, int64_t ld,
+                   void *ws, MxX &o, hipStream_t st) {
+    o = MxX{};
+    o.rows = rows;
+    if (dtype == QMOE_MXFP4) {
+        o.v = static_cast<const uint8_t *>(x);
+        o.s = x_s;
+        o.ld = (int64_t)mx_blocks(cols) * 16;
+        return hipSuccess;
+    }
+    o.width = pad128(cols);
+    if (direct_rows(dtype, cols, ld)) {
+        o.v = static_cast<const uint8_t *>(x);
+        o.ld = ld * 2;
+        return hipSuccess;
+    }
+    o.v = static_cast<const uint8_t *>(ws);
+    o.ld = (int64_t)parts_of(dtype) * o.width * 2;
+    return launch_mx_parts(x, dtype == QMOE_F32, rows, cols, ld, static_cast<uint16_t *>(ws), o.width,
+                           st);
+}
+
+// Which kernel a product takes: passes of 16 rows that stream the weights
+// while groups hold few rows, tiles on the matrix cores otherwise.
+constexpr int STREAM_ROWS = 16;
+bool few_rows(const MxGroups &g) { return g.n <= (int64_t)STREAM_ROWS * g.experts; }
+
+hipError_t product(const MxMat &w, const MxMat &up, const MxX &x, int dtype, const MxGroups &g,
+                   const MxOut &o, hipStream_t st) {
+    const int parts = dtype == QMOE_MXFP4 ? 0 : parts_of(dtype);
+    if (few_rows(g)) return launch_mx_stream(w, up, x, parts, g, o, st);
+    if (parts == 0) return launch_mx_tile_fp4(w, x, g, o, st);
+    return launch_mx_tile(w, up, x, parts, g, o, st);
+}
+
+// Grids stay below 2^31 blocks: tiles (16 rows and more) times column blocks
+// (32 weight rows and more).
+bool grid_fits(int64_t n, int64_t experts, int64_t rows) {
+    return (n / 16 + experts + 1) * (rows / 16 + 1) < LIM31 - 8;
+}
+
+// Checks shared by qmoe_mx_matmul (experts == 0) and qmoe_mx_grouped.
+int product_checks(const qmoe_mxmat *W, int experts, int32_t x_dtype, const void *x,
+                   const uint8_t *x_s, int64_t x_rows, int64_t x_ld, const int32_t *offsets,
+                   const int32_t *pairs, int64_t n, int32_t y_dtype, void *y, int64_t y_ld, void *ws,
+                   size_t ws_bytes) {
+    const int E = experts > 0 ? experts : 1;
+    const int s = check_mxmat(W, E);
+    if (s) return s;
+    if (!float_type(x_dtype) && x_dtype != QMOE_MXFP4) return QMOE_ERR_UNSUPPORTED;
+    if (!float_type(y_dtype)) return QMOE_ERR_UNSUPPORTED;
+    if (x_rows < 0 || n < 0 || x_rows > (1 << 30) || n > (1 << 30)) return QMOE_ERR_SHAPE;
+    if (x_dtype != QMOE_MXFP4 && (x_ld < W->cols || x_ld >> 31)) return QMOE_ERR_SHAPE;
+    if (y_ld < W->rows || y_ld >> 31) return QMOE_ERR_SHAPE;
+    if (!grid_fits(n, E, W->rows)) return QMOE_ERR_SHAPE;
+    if (n == 0) return QMOE_OK;
+    if (x_rows == 0) return QMOE_ERR_SHAPE;
+    if (!x || !y || (x_dtype == QMOE_MXFP4 && !x_s)) return QMOE_ERR_NULL;
+    if (experts > 0 && !offsets) return QMOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(y) || !aligned4(offsets) || !aligned4(pairs)) return QMOE_ERR_ALIGN;
+    if (x_dtype == QMOE_MXFP4 && !aligned16(x_s)) return QMOE_ERR_ALIGN;
+    const int64_t nb = mx_blocks(W->cols);
+    // 32-bit offsets: a gather spans all rows of x, otherwise a tile's rows do
+    const bool dir = direct_rows(x_dtype, W->cols, x_ld);
+    const int64_t row = x_dtype == QMOE_MXFP4 ? nb * 16
+                        : dir                 ? x_ld * 2
+                                              : (int64_t)parts_of(x_dtype) * pad128(W->cols) * 2;
+    if ((pairs ? x_rows : 128) * row >= LIM31) return QMOE_ERR_UNSUPPORTED;
+    const int64_t xb = x_dtype == QMOE_MXFP4 ? x_rows * nb * 16
+                                             : span(x_rows, W->cols, x_ld, elem_bytes(x_dtype));
+    const int64_t xsb = x_dtype == QMOE_MXFP4 ? x_rows * nb : 0;
+    const int64_t yb = span(n, W->rows, y_ld, elem_bytes(y_dtype));
+    const int64_t need = parts_bytes(x_dtype, x_rows, W->cols, x_ld);
+    if (need > 0 && (!ws || (int64_t)ws_bytes < need)) return QMOE_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(ws)) return QMOE_ERR_ALIGN;
+    const int64_t ob = offsets ? 4 * (int64_t)(E + 1) : 0, pb = pairs ? 4 * n : 0;
+    if (overlap(y, yb, x, xb) || overlap(y, yb, x_s, xsb) || overlap(y, yb, offsets, ob) ||
+        overlap(y, yb, pairs, pb) || overlaps_mat(y, yb, W, E) || overlap(y, yb, ws, need) ||
+        overlap(ws, need, x, xb) || overlap(ws, need, offsets, ob) || overlap(ws, need, pairs, pb) ||
+        overlaps_mat(ws, need, W, E))
+        return QMOE_ERR_ALIAS;
+    return QMOE_OK;
+}
+
+int run_product(const qmoe_mxmat *W, int32_t x_dtype, const void *x, const uint8_t *x_s,
+                int64_t x_rows, int64_t x_ld, const MxGroups &g, int32_t y_dtype, void *y,
+                int64_t y_ld, void *ws, hipStream_t st) {
+    MxX o;
+    hipError_t e = operand(x_dtype, x, x_s, x_rows, W->cols, x_ld, ws, o, st);
+    if (e != hipSuccess) return QMOE_ERR_HIP;
+    MxOut out{};
+    out.y = y;
+    out.ld = y_ld;
+    out.type = y_dtype == QMOE_F32 ? MX_OUT_F32 : MX_OUT_BF16;
+    out.vec = W->rows % 4 == 0 && y_ld % 4 == 0;
+    return status_of(product(to_mx(W), MxMat{}, o, x_dtype, g, out, st));
+}
+
+struct MxLayerWs {
+    Worklist wl;
+    int32_t *hist;
+    void *x;             // parts of x (nullptr where x is the operand as it is)
+    uint8_t *h;          // parts of h [pairs][parts][pad128(inter)]
+    float *y;            // weighted expert rows [pairs][hidden]
+    int64_t bytes;
+};
+
+MxLayerWs carve(void *ws, int E, int H, int F, int T, int k, int dtype) {
+    MxLayerWs L{};
+    Carver c(ws);
+    const int64_t n = (int64_t)T * k;
+    L.wl.counts = c.take<int32_t>(E);
+    L.wl.offsets = c.take<int32_t>(E + 1);
+    L.wl.pairs = c.take<int32_t>(n);
+    L.wl.inv = c.take<int32_t>(n);
+    L.wl.n_invalid = c.take<int32_t>(1);
+    L.wl.tile_m = MFMA_BM;
+    L.hist = c.take<int32_t>(wl_scratch_ints(n, E));
+    L.x = c.take<uint8_t>(parts_bytes(dtype, T, H, H));
+    L.h = c.take<uint8_t>(n * parts_of(dtype) * pad128(F) * 2);
+    L.y = c.take<float>(n * H);
+    L.bytes = c.off;
+    return L;
+}
+
+int check_mx_layer(const qmoe_mx_layer_desc *d) {
+    if (!d) return QMOE_ERR_NULL;
+    if (d->struct_size != sizeof(qmoe_mx_layer_desc)) return QMOE_ERR_ABI;
+    if (d->experts < 1 || d->experts > MAX_EXPERTS || d->hidden <= 0 || d->inter <= 0)
+        return QMOE_ERR_SHAPE;
+    const qmoe_mxmat *m[3] = {&d->gate, &d->up, &d->down};
+    for (int i = 0; i < 3; i++) {
+        const int s = check_mxmat(m[i], d->experts);
+        if (s) return s;
+        if (m[i]->rows != (i < 2 ? d->inter : d->hidden) || m[i]->cols != (i < 2 ? d->hidden : d->inter))
+            return QMOE_ERR_SHAPE;
+    }
+    // the padded rows of h and the part rows of x stay within a tile's 32-bit offsets
+    if ((int64_t)128 * 3 * 2 * pad128(d->hidden > d->inter ? d->hidden : d->inter) >= LIM31)
+        return QMOE_ERR_UNSUPPORTED;
+    return QMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qmoe_mx_code_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return 0;
+    return (size_t)(rows * ((cols + 31) / 32) * 16);
+}
+
+size_t qmoe_mx_scale_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return 0;
+    return (size_t)(rows * ((cols + 31) / 32));
+}
+
+static int convert_checks(const void *v, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                          const uint8_t *q, const uint8_t *s) {
+    if (rows < 0 || cols < 0 || cols >> 31 || ld < cols || ld >> 31 || rows >> 40) return QMOE_ERR_SHAPE;
+    if (!float_type(dtype)) return QMOE_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return QMOE_OK;
+    if (!v || !q || !s) return QMOE_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(v) % elem_bytes(dtype) || !aligned16(q)) return QMOE_ERR_ALIGN;
+    const int64_t vb = span(rows, cols, ld, elem_bytes(dtype));
+    const int64_t qb = (int64_t)qmoe_mx_code_bytes(rows, cols), sb = qb / 16;
+    if (overlap(v, vb, q, qb) || overlap(v, vb, s, sb) || overlap(q, qb, s, sb)) return QMOE_ERR_ALIAS;
+    return QMOE_OK;
+}
+
+int qmoe_mx_quantize(const void *x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t x_ld,
+                     uint8_t *q, uint8_t *s, void *stream) {
+    const int c = convert_checks(x, x_dtype, rows, cols, x_ld, q, s);
+    if (c || rows == 0 || cols == 0) return c;
+    return status_of(launch_mx_quantize(x, x_dtype == QMOE_F32, rows, (int)cols, x_ld, q, s,
+                                        as_stream(stream)));
+}
+
+int qmoe_mx_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols, void *y,
+                       int32_t y_dtype, int64_t y_ld, void *stream) {
+    const int c = convert_checks(y, y_dtype, rows, cols, y_ld, q, s);
+    if (c || rows == 0 || cols == 0) return c;
+    return status_of(launch_mx_dequantize(q, s, rows, (int)cols, y, y_dtype == QMOE_F32, y_ld,
+                                          as_stream(stream)));
+}
+
+size_t qmoe_mx_workspace_bytes(const qmoe_mxmat *W, int32_t x_dtype, int32_t x_rows, int64_t x_ld) {
+    if (!W || W->cols <= 0 || x_rows < 0 || x_ld < 0) return 0;
+    if (!float_type(x_dtype)) return 0;
+    return (size_t)parts_bytes(x_dtype, x_rows, W->cols, x_ld);
+}
+
+int qmoe_mx_matmul(const qmoe_mxmat *W, int32_t x_dtype, const void *x, const uint8_t *x_s,
+                   int32_t batch, int64_t x_ld, int32_t y_dtype, void *y, int64_t y_ld, void *ws,
+                   size_t ws_bytes, void *stream) {
+    const int s = product_checks(W, 0, x_dtype, x, x_s, batch, x_ld, nullptr, nullptr, batch, y_dtype,
+                                 y, y_ld, ws, ws_bytes);
+    if (s || batch == 0) return s;
+    MxGroups g{};
+    g.k = 1;
+    g.experts = 1;
+    g.n = batch;
+    return run_product(W, x_dtype, x, x_s, batch, x_ld, g, y_dtype, y, y_ld, ws, as_stream(stream));
+}
+
+int qmoe_mx_grouped(const qmoe_mxmat *W, int32_t experts, int32_t x_dtype, const void *x,
+                    const uint8_t *x_s, int32_t x_rows, int64_t x_ld, const int32_t *offsets,
+                    const int32_t *pairs, int32_t k, int32_t n, int32_t y_dtype, void *y,
+                    int64_t y_ld, void *ws, size_t ws_bytes, void *stream) {
+    if (experts < 1 || experts > MAX_EXPERTS || k < 1) return QMOE_ERR_SHAPE;
+    if (!pairs && x_rows < n) return QMOE_ERR_SHAPE;
+    const int s = product_checks(W, experts, x_dtype, x, x_s, x_rows, x_ld, offsets, pairs, n, y_dtype,
+                                 y, y_ld, ws, ws_bytes);
+    if (s || n == 0) return s;
+    MxGroups g{};
+    g.offsets = offsets;
+    g.pairs = pairs;
+    g.k = k;
+    g.experts = experts;
+    g.n = n;
+    return run_product(W, x_dtype, x, x_s, x_rows, x_ld, g, y_dtype, y, y_ld, ws, as_stream(stream));
+}
+
+size_t qmoe_mx_layer_workspace_bytes(const qmoe_mx_layer_desc *desc, int32_t tokens, int32_t k,
+                                     int32_t x_dtype) {
+    if (!desc || tokens < 0 || k < 1 || k > MAX_TOPK || desc->experts < 1 || desc->hidden < 1 ||
+        desc->inter < 1 || !float_type(x_dtype))
+        return 0;
+    return (size_t)carve(nullptr, desc->experts, desc->hidden, desc->inter, tokens, k, x_dtype).bytes;
+}
+
+int qmoe_mx_layer(const qmoe_mx_layer_desc *desc, int32_t x_dtype, const void *x, int32_t tokens,
+                  const int32_t *topk_ids, const float *topk_w, int32_t k, void *out, void *ws,
+                  size_t ws_bytes, void *stream) {
+    const int s = check_mx_layer(desc);
+    if (s) return s;
+    if (!float_type(x_dtype)) return QMOE_ERR_UNSUPPORTED;
+    if (tokens < 0 || k < 1 || k > MAX_TOPK || (int64_t)tokens * k > (1 << 30)) return QMOE_ERR_SHAPE;
+    const int E = desc->experts, H = desc->hidden, F = desc->inter;
+    const int64_t n = (int64_t)tokens * k;
+    if (!grid_fits(n, E, H > F ? H : F)) return QMOE_ERR_SHAPE;
+    const int64_t xrow = direct_rows(x_dtype, H, H) ? 2 * (int64_t)H
+                                                    : (int64_t)parts_of(x_dtype) * pad128(H) * 2;
+    if (tokens * xrow >= LIM31) return QMOE_ERR_UNSUPPORTED;
+    if (tokens == 0) return QMOE_OK;
+    if (!x || !topk_ids || !topk_w || !out) return QMOE_ERR_NULL;
+    if (!aligned16(x) || !aligned16(out) || !aligned4(topk_ids) || !aligned4(topk_w))
+        return QMOE_ERR_ALIGN;
+    const MxLayerWs L = carve(ws, E, H, F, tokens, k, x_dtype);
+    if (!ws || (int64_t)ws_bytes < L.bytes) return QMOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QMOE_ERR_ALIGN;
+    const int64_t xb = (int64_t)tokens * H * elem_bytes(x_dtype);
+    if (overlap(out, xb, x, xb) || overlap(out, xb, topk_ids, 4 * n) || overlap(out, xb, topk_w, 4 * n) ||
+        overlap(out, xb, ws, L.bytes) || overlap(ws, L.bytes, x, xb) ||
+        overlap(ws, L.bytes, topk_ids, 4 * n) || overlap(ws, L.bytes, topk_w, 4 * n))
+        return QMOE_ERR_ALIAS;
+    const qmoe_mxmat *m[3] = {&desc->gate, &desc->up, &desc->down};
+    for (const qmoe_mxmat *a : m)
+        if (overlaps_mat(out, xb, a, E) || overlaps_mat(ws, L.bytes, a, E)) return QMOE_ERR_ALIAS;
+
+    const hipStream_t st = as_stream(stream);
+    hipError_t e = launch_worklist(topk_ids, (int)n, k, E, L.wl, L.hist, st);
+    MxX xo;
+    if (e == hipSuccess) e = operand(x_dtype, x, nullptr, tokens, H, H, L.x, xo, st);
+    MxGroups g{};
+    g.offsets = L.wl.offsets;
+    g.pairs = L.wl.pairs;
+    g.k = k;
+    g.experts = E;
+    g.n = (int)n;
+    MxOut h{};
+    h.y = L.h;
+    h.width = pad128(F);
+    h.ld = (int64_t)parts_of(x_dtype) * h.width * 2;
+    if (e == hipSuccess) e = product(to_mx(&desc->gate), to_mx(&desc->up), xo, x_dtype, g, h, st);
+    MxX ho{};
+    ho.v = L.h;
+    ho.ld = h.ld;
+    ho.rows = n;
+    ho.width = h.width;
+    g.pairs = nullptr;
+    MxOut y{};
+    y.y = L.y;
+    y.ld = H;
+    y.type = MX_OUT_F32;
+    y.w = topk_w;
+    y.wpairs = L.wl.pairs;
+    y.vec = H % 4 == 0;
+    if (e == hipSuccess) e = product(to_mx(&desc->down), MxMat{}, ho, x_dtype, g, y, st);
+    if (e == hipSuccess)
+        e = launch_mx_combine(L.y, L.wl.inv, tokens, k, H, out, x_dtype == QMOE_F32, st);
+    return status_of(e);
+}
+
+}  // extern "C"

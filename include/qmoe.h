@@ -113,6 +113,9 @@ enum {
  * paths. */
 enum { QMOE_F32 = 0, QMOE_BF16 = 1, QMOE_F32_DIGITS = 2 };
 
+/* Type of MXFP4 rows as an operand of the qmoe_mx_* products (see below). */
+enum { QMOE_MXFP4 = 3 };
+
 /* One grouped int4 matrix, or a stack of per-expert matrices of one shape.
  * q_expert_stride is the byte distance between experts' packed codes and
  * s_expert_stride the float distance between their scales (0 for a single
@@ -452,6 +455,108 @@ int qmoe_layer_ws_layout(const qmoe_layer_desc *desc, int32_t tokens,
 int qmoe_layer_noalloc(const qmoe_layer_desc *desc, int32_t x_dtype, const void *x,
                        int32_t tokens, const int32_t *topk_ids, const float *topk_w,
                        int32_t k, float *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4: microscaled 4-bit floats beside the int4 container.  A row of `cols`
+ * values is stored in nb = ceil(cols / 32) whole blocks of 32: codes
+ * [rows][nb][16] bytes (element 2j of a block in the low nibble of byte j)
+ * and scales [rows][nb] bytes.  A code holds a sign bit, two exponent bits and
+ * one mantissa bit (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6); a scale byte c
+ * stands for 2^(c - 127), 255 for NaN.  A value is code times scale.  Elements
+ * of the last block past `cols` have to be code 0 where both operands of a
+ * product are MXFP4; elsewhere they are not used.
+ * The conventions above hold (device pointers, checks before any launch, no
+ * allocation, 16-byte alignment); widths and row counts are free.  A matrix's
+ * codes stay below 2 GB (QMOE_ERR_UNSUPPORTED).
+ *
+ * Arithmetic of the products: MXFP4 values are exact in bf16; a bf16 row is
+ * multiplied as it is, an f32 row as three bf16 parts that sum to it exactly
+ * (bits below 2^-133 are lost), an MXFP4 row by the scaled 4-bit matrix
+ * instructions.  Products are exact and sums are f32.  A NaN or infinity in x
+ * or a NaN block reaches every output it feeds.  Results do not change from
+ * run to run (no atomics). */
+
+/* rows * nb * 16 and rows * nb: bytes of codes and scales (0 for negative
+ * sizes). */
+size_t qmoe_mx_code_bytes(int64_t rows, int64_t cols);
+size_t qmoe_mx_scale_bytes(int64_t rows, int64_t cols);
+
+/* Round rows to MXFP4.  x [rows][cols] of x_dtype (QMOE_F32 or QMOE_BF16),
+ * x_ld >= cols elements between rows, aligned to its element; q 16-byte
+ * aligned; s any.  Per block: E = max(floor(log2(max |x|)) - 2, -127), scale
+ * byte E + 127, each element x / 2^E rounded to the nearest code, ties to the
+ * even one, at most 6 in magnitude; a block of zeros takes scale byte 0; a
+ * block with a NaN or an infinity becomes NaN (scale byte 255, codes 0).  The
+ * elements past cols are stored as code 0.  Bit-exact. */
+int qmoe_mx_quantize(const void *x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t x_ld,
+                     uint8_t *q, uint8_t *s, void *stream);
+
+/* MXFP4 rows back to f32 or bf16 values (exact, but for magnitudes of 2^128
+ * and more, which become infinite); y [rows][cols], y_ld >= cols elements
+ * between rows, aligned to its element. */
+int qmoe_mx_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int64_t cols, void *y,
+                       int32_t y_dtype, int64_t y_ld, void *stream);
+
+/* One MXFP4 matrix [rows][cols], or a stack of per-expert matrices of one
+ * shape; the expert strides are in bytes, the codes' a multiple of 16. */
+typedef struct qmoe_mxmat {
+    uint32_t struct_size;     /* = sizeof(qmoe_mxmat) */
+    int32_t rows;             /* output features */
+    int32_t cols;             /* input features */
+    const uint8_t *q;         /* codes, [E][rows][nb][16] */
+    const uint8_t *s;         /* scales, [E][rows][nb] */
+    int64_t q_expert_stride;  /* bytes between experts' codes */
+    int64_t s_expert_stride;  /* bytes between experts' scales */
+} qmoe_mxmat;
+
+/* Workspace bytes of qmoe_mx_matmul and qmoe_mx_grouped for x_rows rows of x,
+ * x_ld elements apart: the bf16 parts of f32 rows, and of bf16 rows whose
+ * width is not a multiple of 128 or whose x_ld is not a multiple of 8; 0 for
+ * other bf16 rows and for MXFP4 rows. */
+size_t qmoe_mx_workspace_bytes(const qmoe_mxmat *W, int32_t x_dtype, int32_t x_rows, int64_t x_ld);
+
+/* y[b][o] = sum_i W[o][i] x[b][i] for b < batch: the product with one MXFP4
+ * matrix (expert 0 of W).  x_dtype QMOE_F32, QMOE_BF16 (x_ld elements between
+ * rows) or QMOE_MXFP4 (x the codes, x_s the scales of batch rows as
+ * qmoe_mx_quantize writes them; x_ld ignored); y f32 or bf16 per y_dtype, y_ld
+ * elements between rows.  y may not overlap anything else, the gaps of strided
+ * rows included. */
+int qmoe_mx_matmul(const qmoe_mxmat *W, int32_t x_dtype, const void *x, const uint8_t *x_s,
+                   int32_t batch, int64_t x_ld, int32_t y_dtype, void *y, int64_t y_ld, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* Products grouped by expert: rows offsets[e] <= r < offsets[e + 1] of y are
+ * y[r] = W_e x[src(r)], with src(r) = pairs[r] / k, or r when pairs is NULL.
+ * offsets (int32 [experts + 1], device) and pairs (int32 [n], device) are what
+ * qmoe_worklist leaves; offsets must not decrease and are clamped to [0, n].
+ * Rows of y that no group holds are left as they were; a row whose pair names
+ * no row of x is written as zeros.  x has x_rows rows (at least n without
+ * pairs; with pairs its operand rows must span less than 2 GB, else
+ * QMOE_ERR_UNSUPPORTED).  No host round trip: group sizes are read on the
+ * device. */
+int qmoe_mx_grouped(const qmoe_mxmat *W, int32_t experts, int32_t x_dtype, const void *x,
+                    const uint8_t *x_s, int32_t x_rows, int64_t x_ld, const int32_t *offsets,
+                    const int32_t *pairs, int32_t k, int32_t n, int32_t y_dtype, void *y,
+                    int64_t y_ld, void *ws, size_t ws_bytes, void *stream);
+
+/* The routed layer with MXFP4 experts:
+ *   out[t] = sum_{j<k} topk_w[t][j] * down_e(silu(gate_e x_t) * (up_e x_t)),
+ * e = topk_ids[t][j]; gate and up [E][inter][hidden], down [E][hidden][inter],
+ * any widths.  x is [tokens][hidden] f32 or bf16 and out has x's type.  With
+ * f32 rows h stays f32 (its exact parts feed the down projection); with bf16
+ * rows h is rounded to bf16; sums are f32 and out is rounded once.  Ids outside
+ * [0, E) are dropped.  k <= 64.  out is fully written and must not overlap
+ * anything else.  x's operand rows must span less than 2 GB. */
+typedef struct qmoe_mx_layer_desc {
+    uint32_t struct_size;     /* = sizeof(qmoe_mx_layer_desc) */
+    int32_t experts, hidden, inter;
+    qmoe_mxmat gate, up, down;
+} qmoe_mx_layer_desc;
+size_t qmoe_mx_layer_workspace_bytes(const qmoe_mx_layer_desc *desc, int32_t tokens, int32_t k,
+                                     int32_t x_dtype);
+int qmoe_mx_layer(const qmoe_mx_layer_desc *desc, int32_t x_dtype, const void *x, int32_t tokens,
+                  const int32_t *topk_ids, const float *topk_w, int32_t k, void *out, void *ws,
+                  size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
