@@ -48,6 +48,30 @@ __device__ __forceinline__ void mxt_interleave() {
     }
 }
 
+// Four consecutive outputs n .. n + 3 (below `rows`) of row `pos` of y.
+__device__ __forceinline__ void mxt_put4(const MxOut &o, int64_t pos, int n, int rows,
+                                         const float v[4]) {
+    const int64_t at = pos * o.ld + n;
+    if (o.vec) {
+        if (n >= rows) return;               // rows is a multiple of 4 here
+        if (o.type == MX_OUT_F32) {
+            __builtin_memcpy(__builtin_assume_aligned(static_cast<float *>(o.y) + at, 16), v, 16);
+        } else {
+            uint16_t b[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) b[r] = mx_bf16(v[r]);
+            __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t *>(o.y) + at, 8), b, 8);
+        }
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        if (n + r >= rows) continue;
+        if (o.type == MX_OUT_F32) static_cast<float *>(o.y)[at + r] = v[r];
+        else static_cast<uint16_t *>(o.y)[at + r] = mx_bf16(v[r]);
+    }
+}
+
 // Writes the accumulators of a wave.  acc[i][j][4 q + r]: x row 32 i +
 // lane % 32 of the tile, weight row 8 q + 4 (lane / 32) + r of operand j.
 template <int TF, int PARTS, bool PAIR>
@@ -99,24 +123,7 @@ __device__ __forceinline__ void mxt_store(const f32x16 (&acc)[TF][MXT_WF], const
                     float v[4];
 #pragma unroll
                     for (int r = 0; r < 4; r++) v[r] = none ? 0.0f : acc[i][j][4 * q + r] * f;
-                    const int64_t at = pos * o.ld + n;
-                    if (o.vec && n < rows_w) {
-                        if (o.type == MX_OUT_F32) {
-                            __builtin_memcpy(__builtin_assume_aligned(static_cast<float *>(o.y) + at, 16), v, 16);
-                        } else {
-                            uint16_t b[4];
-#pragma unroll
-                            for (int r = 0; r < 4; r++) b[r] = mx_bf16(v[r]);
-                            __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t *>(o.y) + at, 8), b, 8);
-                        }
-                    } else if (!o.vec) {
-#pragma unroll
-                        for (int r = 0; r < 4; r++) {
-                            if (n + r >= rows_w) continue;
-                            if (o.type == MX_OUT_F32) static_cast<float *>(o.y)[at + r] = v[r];
-                            else static_cast<uint16_t *>(o.y)[at + r] = mx_bf16(v[r]);
-                        }
-                    }
+                    mxt_put4(o, pos, n, rows_w, v);
                 }
             }
         }
