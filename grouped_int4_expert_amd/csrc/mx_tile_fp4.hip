@@ -54,7 +54,10 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_fp4_kernel(MxMat W, Mx
     constexpr int XL = XF >= 4 ? XF / 4 : 1; // x loads of a wave per stage (16 rows each)
     constexpr int LOADS = XL + WF;
     constexpr int AHEAD = 2;                 // stages in flight beyond the one computed
-    __shared__ __attribute__((aligned(1024))) uint8_t sx[4][XROWS * 64];
+    static_assert(AHEAD == 2, "the stages' arrays below");
+    // one array per stage: reads of a stage then do not wait for loads into another
+    __shared__ __attribute__((aligned(1024))) uint8_t sx0[XROWS * 64], sx1[XROWS * 64],
+        sx2[XROWS * 64], sx3[XROWS * 64];
     __shared__ __attribute__((aligned(16))) uint8_t panel[(XROWS + FP_WROWS) * FP_PITCH];
     const int nb = W.nb;
     const int ncb = (W.rows + FP_WROWS - 1) / FP_WROWS;
@@ -98,41 +101,58 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_fp4_kernel(MxMat W, Mx
     const int iters = (nb + 3) / 4;
     u32x4 rq[4][WF];
     uint32_t sw[WF], sc[XF];
-    auto issue = [&](int it, int slot) {
+    auto issue = [&](int it, int slot, uint8_t *sx) {
         const int gi = min(it, iters - 1);
         // blocks past a row read as code 0 in x; what the weights hold there is
         // finite (their panel scales are 0, which stands for 2^-127)
         const bool out = 4 * gi + piece >= nb;
 #pragma unroll
         for (int i = 0; i < XL; i++)
-            mxt_load_lds(xr, sx[slot] + (i + XL * w) * 1024 % (XROWS * 64), out ? OOB_OFFSET : xoff[i] + gi * 64, 0);
+            mxt_load_lds(xr, sx + (i + XL * w) * 1024 % (XROWS * 64),
+                         out ? OOB_OFFSET : xoff[i] + gi * 64, 0);
 #pragma unroll
         for (int j = 0; j < WF; j++)
             rq[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(wr, woff[j], gi * 64, 0);
     };
     const int xpiece = fp_slot(r16, quarter) * 16;
-#define FP_STAGE(it, s)                                                                           \
+#define FP_STAGE(s, cur, ahead)                                                                          \
     {                                                                                             \
         __builtin_amdgcn_s_waitcnt(waitcnt_vm((AHEAD - 1) * LOADS));                              \
         __builtin_amdgcn_s_barrier();                                                             \
-        issue((it) + AHEAD, ((s) + AHEAD) & 3);                                                   \
-        if ((it) < last) {                                                                        \
-            i32x8 wb[WF];                                                                         \
-            _Pragma("unroll") for (int j = 0; j < WF; j++) {                                      \
-                const u32x4 c = rq[s][j];                                                         \
-                wb[j] = i32x8{(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};            \
-            }                                                                                     \
+        issue((s) + AHEAD < 4 ? it + (s) + AHEAD : next + (s) + AHEAD - 4, ((s) + AHEAD) & 3,     \
+              ahead);                                                                             \
+        if (it + (s) < last) {                                                                    \
+            u32x4 xc[XF];                                                                         \
+            _Pragma("unroll") for (int i = 0; i < XF; i++) xc[i] =                                \
+                *reinterpret_cast<const u32x4 *>(&cur[(16 * i + r16) * 64 + xpiece]);           \
             _Pragma("unroll") for (int i = 0; i < XF; i++) {                                      \
-                const u32x4 c =                                                                   \
-                    *reinterpret_cast<const u32x4 *>(&sx[s][(16 * i + r16) * 64 + xpiece]);       \
-                const i32x8 xb = {(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};        \
-                _Pragma("unroll") for (int j = 0; j < WF; j++) acc[i][j] =                        \
-                    __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                             \
-                        wb[j], xb, acc[i][j], 4, 4, s, (int)sw[j], s, (int)sc[i]);                \
+                const i32x8 xb = {(int)xc[i][0], (int)xc[i][1], (int)xc[i][2], (int)xc[i][3],     \
+                                  0, 0, 0, 0};                                                    \
+                _Pragma("unroll") for (int j = 0; j < WF; j++) {                                  \
+                    const u32x4 c = rq[s][j];                                                     \
+                    const i32x8 wb = {(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};    \
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                 \
+                        wb, xb, acc[i][j], 4, 4, s, (int)sw[j], s, (int)sc[i]);                   \
+                }                                                                                 \
             }                                                                                     \
+            __builtin_amdgcn_sched_group_barrier(0x100, XF, 0);                                   \
+            __builtin_amdgcn_sched_group_barrier(0x008, XF * WF, 0);                              \
         }                                                                                         \
     }
-    for (int p0 = 0; p0 < nb; p0 += FP_PANEL) {
+    // Rows lie a power of two apart at the usual widths, so the same inputs of
+    // all rows come from one or two of the L2's 16 channels: blocks that walked
+    // the inputs in the same order would all queue there.  Each column block
+    // and matrix starts at another quadruple of stages of another panel (the
+    // tiles of one matrix in step: they share its weights).
+    const int panels = (nb + FP_PANEL - 1) / FP_PANEL, turn = t.cb + t.e;
+    for (int p = 0; p < panels; p++) {
+        const int p0 = (p + turn) % panels * FP_PANEL;
+        const int it0 = p0 / 4, last = min(iters, it0 + FP_PANEL / 4);
+        const int quads = (last - it0 + 3) / 4;
+        int quad = turn / panels % quads;
+        int it = it0 + 4 * quad;
+        issue(it, 0, sx0);
+        issue(it + 1, 1, sx1);
         const int chunks = (min(nb - p0, FP_PANEL) + 15) / 16;      // of 16 blocks per row
         for (int c = threadIdx.x; c < (XROWS + FP_WROWS) * chunks; c += MXT_THREADS) {
             const int row = c / chunks, b = (c - row * chunks) * 16;
@@ -142,14 +162,13 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_fp4_kernel(MxMat W, Mx
                       (int64_t)min(t.cb * FP_WROWS + row - XROWS, W.rows - 1) * nb;
             fp_panel16(panel + row * FP_PITCH, src, p0 + b, b, nb);
         }
-        const int it0 = p0 / 4, last = min(iters, it0 + FP_PANEL / 4);
-#pragma unroll
-        for (int a = 0; a < AHEAD; a++) issue(it0 + a, a);
         // the stages in flight: all of them, the compiler may order their loads
         // among each other here
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         __syncthreads();
-        for (int it = it0; it < last; it += 4) {
+        for (int k = 0; k < quads; k++) {
+            quad = quad + 1 == quads ? 0 : quad + 1;
+            const int next = it0 + 4 * quad;
             const int at = quarter * (FP_PANEL / 4) + (it - it0);
 #pragma unroll
             for (int j = 0; j < WF; j++)
@@ -158,10 +177,11 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_fp4_kernel(MxMat W, Mx
 #pragma unroll
             for (int i = 0; i < XF; i++)
                 sc[i] = *reinterpret_cast<const uint32_t *>(panel + (16 * i + r16) * FP_PITCH + at);
-            FP_STAGE(it, 0)
-            FP_STAGE(it + 1, 1)
-            FP_STAGE(it + 2, 2)
-            FP_STAGE(it + 3, 3)
+            FP_STAGE(0, sx0, sx2)
+            FP_STAGE(1, sx1, sx3)
+            FP_STAGE(2, sx2, sx0)
+            FP_STAGE(3, sx3, sx1)
+            it = next;
         }
         // no load may still write LDS and no wave read the panel when the next
         // panel (or the end) comes
