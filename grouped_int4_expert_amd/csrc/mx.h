@@ -77,6 +77,32 @@ __device__ __forceinline__ u32x4 mx_decode8(uint32_t d, float scale) {
     return r.v;
 }
 
+// Scale bytes b0 .. b0 + 15 of a row of nb, 0 past its end (which stands for
+// 2^-127; what it multiplies there is 0 in x).
+__device__ __forceinline__ u32x4 mx_scales16(const uint8_t *row, int b0, int nb) {
+    u32x4 v;
+    if (b0 + 16 <= nb) {
+        __builtin_memcpy(&v, row + b0, 16);
+    } else {
+        uint64_t part[2] = {0, 0};
+#pragma unroll 1
+        for (int j = 0; b0 + j < nb; j++) {
+            const uint64_t c = (uint64_t)row[b0 + j] << (8 * (j & 7));
+            if (j < 8) part[0] |= c;
+            else part[1] |= c;
+        }
+        __builtin_memcpy(&v, part, 16);
+    }
+    return v;
+}
+
+// Byte q of each dword: the scales of block q of four consecutive stages, the
+// byte of stage s at place s.
+__device__ __forceinline__ uint32_t mx_pick(u32x4 v, int q) {
+    const uint32_t sel = 0x0c0c0400u + 0x0101u * q;
+    return perm_b32(v[1], v[0], sel) | perm_b32(v[3], v[2], sel) << 16;
+}
+
 // f32 as three bf16 parts, exact: each part takes the top 8 significant bits
 // that are left (truncation), 3 x 8 = 24.  A NaN or infinity goes into the
 // first part alone (inf - inf would make a NaN of it).  Bits below 2^-133

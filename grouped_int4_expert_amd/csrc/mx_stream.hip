@@ -2,24 +2,104 @@
 // pass of at most 16 rows.
 //
 // A block takes RT row tiles of 16 weight rows and one pass; its waves split
-// the inputs (wave w takes the 128-input steps w, w + WV, ...) and meet in
-// LDS at the end.  In a step a lane holds one whole block of a weight row
-// (row lane % 16, block lane / 16: 16 bytes of codes and the scale byte), so
-// the codes go from memory to the matrix cores through registers only:
+// the inputs into chunks of 512 (wave w takes chunks w, w + WV, ...) and meet
+// in LDS at the end.  A chunk is four steps of 128 inputs; in a step a lane
+// holds one whole block of a weight row (row lane % 16, block lane / 16: 16
+// bytes of codes), and the 16 scale bytes of the row's chunk come in one load
+// of which each lane picks its four.  The codes go from memory to the matrix
+// cores through registers only:
 //  * bf16 parts: dword j of the block is decoded to 8 exact bf16 values and
 //    multiplied with inputs 32 b + 8 j .. + 7 of the same block b of x
 //    (16x16x32 MFMA; the order of the products inside a sum is free, so both
 //    operands may take their inputs in this order).  Products are exact, sums
-//    f32; the three parts of an f32 row go into one accumulator.
+//    f32.  The three parts of up to five f32 rows lie side by side in the 16
+//    columns of one MFMA; of more rows they go into one accumulator in turn.
 //  * MXFP4 x: the scaled 16x16x128 MFMA takes both blocks and their scale
 //    bytes as they are.
 // The x operand is read straight from global memory (a pass's rows stay in
-// L2).  Columns past the pass read its first row and are not stored.
+// L2); RT sets how often: what bounds this kernel, beside memory, is the
+// number of load instructions.  Columns past the pass read its last row and
+// are not stored.
 #include "mx.h"
 
 namespace qmoe {
 
-constexpr int MXS_ROWS = 16;   // rows per pass
+constexpr int MXS_ROWS = 16;    // rows per pass
+constexpr int MXS_WIDE_ROWS = 32;   // up to here blocks take two tiles, above four
+constexpr int MXS_PACK = 5;     // f32 rows whose parts share the 16 columns
+
+template <int RT>
+struct MxsWeights {
+    const uint8_t *q[RT], *s[RT];
+};
+
+// acc[i] += tile i of the weights times x over the wave's chunks.  NP parts of
+// x (`part` bytes apart) go into the same accumulators; 0: x is MXFP4.
+template <int NP, int RT, int WV>
+__device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> &W,
+                                         const uint8_t *xv, const uint8_t *xs, int64_t part, int nb,
+                                         int w) {
+    constexpr int P = NP == 0 ? 1 : NP;
+    const int quarter = lane_id() >> 4;
+    const int chunks = (nb + 15) / 16;
+    for (int c = w; c < chunks; c += WV) {
+        u32x4 cq[4][RT];
+        uint32_t cs[RT], xc = 0;
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
+            const u32x4 v = mx_scales16(W.s[i], 16 * c, nb);
+#pragma unroll
+            for (int s = 0; s < 4; s++) {
+                // blocks past the row re-read its last: finite codes times zeros of x
+                const int b = min(16 * c + 4 * s + quarter, nb - 1);
+                cq[s][i] = *reinterpret_cast<const u32x4 *>(W.q[i] + (int64_t)b * 16);
+            }
+            cs[i] = mx_pick(v, quarter);
+        }
+        if constexpr (NP == 0) xc = mx_pick(mx_scales16(xs, 16 * c, nb), quarter);
+#pragma unroll
+        for (int s = 0; s < 4; s++) {
+            const int b = 16 * c + 4 * s + quarter;
+            if constexpr (NP == 0) {
+                u32x4 xq = *reinterpret_cast<const u32x4 *>(xv + (int64_t)min(b, nb - 1) * 16);
+                if (b >= nb) xq = u32x4{0, 0, 0, 0};
+                const i32x8 xb = {(int)xq[0], (int)xq[1], (int)xq[2], (int)xq[3], 0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < RT; i++) {
+                    const u32x4 e = cq[s][i];
+                    const i32x8 wb = {(int)e[0], (int)e[1], (int)e[2], (int)e[3], 0, 0, 0, 0};
+#define MXS_STEP(n)                                                                               \
+    if (s == n)                                                                                   \
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, xb, acc[i], 4, 4, n,        \
+                                                                  (int)cs[i], n, (int)xc);
+                    MXS_STEP(0) MXS_STEP(1) MXS_STEP(2) MXS_STEP(3)
+#undef MXS_STEP
+                }
+            } else {
+                // x rows hold zeros up to a whole step past their end; the steps
+                // after that are not computed
+                if (16 * c + 4 * s >= nb) break;
+                bf16x8 xf[P][4];
+#pragma unroll
+                for (int p = 0; p < P; p++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        xf[p][j] = *reinterpret_cast<const bf16x8 *>(xv + p * part + (int64_t)b * 64 + j * 16);
+#pragma unroll
+                for (int i = 0; i < RT; i++) {
+                    const float sc = mx_scale((cs[i] >> (8 * s)) & 255u);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const bf16x8 wf = __builtin_bit_cast(bf16x8, mx_decode8(cq[s][i][j], sc));
+#pragma unroll
+                        for (int p = 0; p < P; p++)
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[p][j], acc[i], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+}
 
 // parts: 0, 1, 3; PAIR: tiles RT/2.. are of the second matrix (up) and the
 // block writes h = silu(g) * u.
@@ -27,81 +107,40 @@ template <int PARTS, int RT, int WV, bool PAIR>
 __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, MxX x, MxGroups g,
                                                             MxOut o) {
     constexpr int RTM = PAIR ? RT / 2 : RT;      // tiles of one matrix
-    constexpr int P = PARTS == 0 ? 1 : PARTS;
     __shared__ __attribute__((aligned(16))) float red[WV][RT][64][4];
     const int ncb = ((PAIR ? o.width : W.rows) + 16 * RTM - 1) / (16 * RTM);
     MxTile t;
     if (!mx_find(g, MXS_ROWS, ncb, t)) return;
     const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
-    const int r16 = lane & 15, quarter = lane >> 4;
+    const int r16 = lane & 15;
     const int o0 = t.cb * 16 * RTM;
 
-    // this lane's x row
-    const int col = min(r16, t.rows - 1);
-    int64_t src = mx_source(g, x, t.pos0 + col);
-    const uint8_t *xv = x.v + (src < 0 ? 0 : src) * x.ld;
-    const uint8_t *xs = PARTS == 0 ? x.s + (src < 0 ? 0 : src) * W.nb : nullptr;
+    // this lane's x row, and with packed parts its part
+    const bool packed = PARTS == 3 && t.rows <= MXS_PACK;
+    const int part = packed ? min(r16 / MXS_PACK, 2) : 0;
+    const int col = min(packed ? r16 % MXS_PACK : r16, t.rows - 1);
+    const int64_t src = max(mx_source(g, x, t.pos0 + col), (int64_t)0);
+    const uint8_t *xv = x.v + src * x.ld + (int64_t)part * x.width * 2;
+    const uint8_t *xs = PARTS == 0 ? x.s + src * W.nb : nullptr;
 
-    const uint8_t *wq[RT], *wsc[RT];
+    MxsWeights<RT> wt;
 #pragma unroll
     for (int i = 0; i < RT; i++) {
         const bool second = PAIR && i >= RTM;
         const MxMat &M = second ? U : W;
         const int row = min(o0 + 16 * (i - (second ? RTM : 0)) + r16, M.rows - 1);
-        wq[i] = M.q + (int64_t)t.e * M.q_stride + (int64_t)row * M.nb * 16;
-        wsc[i] = M.s + (int64_t)t.e * M.s_stride + (int64_t)row * M.nb;
+        wt.q[i] = M.q + (int64_t)t.e * M.q_stride + (int64_t)row * M.nb * 16;
+        wt.s[i] = M.s + (int64_t)t.e * M.s_stride + (int64_t)row * M.nb;
     }
 
     f32x4 acc[RT];
 #pragma unroll
     for (int i = 0; i < RT; i++) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int nb = W.nb, steps = (nb + 3) / 4;
-    for (int st = w; st < steps; st += WV) {
-        const int b = 4 * st + quarter;
-        const bool in = b < nb;            // blocks past the row: code 0
-        const int bc = in ? b : nb - 1;
-        u32x4 cq[RT];
-        uint32_t cs[RT];
-#pragma unroll
-        for (int i = 0; i < RT; i++) {
-            cq[i] = *reinterpret_cast<const u32x4 *>(wq[i] + (int64_t)bc * 16);
-            cs[i] = wsc[i][bc];
-        }
-        if constexpr (PARTS == 0) {
-            u32x4 xq = *reinterpret_cast<const u32x4 *>(xv + (int64_t)bc * 16);
-            const uint32_t xc = xs[bc];
-            if (!in) xq = u32x4{0, 0, 0, 0};
-            const i32x8 xb = {(int)xq[0], (int)xq[1], (int)xq[2], (int)xq[3], 0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < RT; i++) {
-                if (!in) cq[i] = u32x4{0, 0, 0, 0};
-                const i32x8 wb = {(int)cq[i][0], (int)cq[i][1], (int)cq[i][2], (int)cq[i][3], 0, 0, 0, 0};
-                acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    wb, xb, acc[i], 4, 4, 0, in ? (int)cs[i] : 127, 0, in ? (int)xc : 127);
-            }
-        } else {
-            // x rows are padded to whole steps (zeros), so b needs no bound there
-            bf16x8 xf[P][4];
-#pragma unroll
-            for (int p = 0; p < P; p++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    xf[p][j] = *reinterpret_cast<const bf16x8 *>(xv + (int64_t)p * x.width * 2 +
-                                                                 (int64_t)b * 64 + j * 16);
-#pragma unroll
-            for (int i = 0; i < RT; i++) {
-                // a block past the row: finite codes times the zeros of x
-                const float sc = in ? mx_scale(cs[i]) : 1.0f;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const bf16x8 wf = __builtin_bit_cast(bf16x8, mx_decode8(cq[i][j], sc));
-#pragma unroll
-                    for (int p = 0; p < P; p++)
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[p][j], acc[i], 0, 0, 0);
-                }
-            }
-        }
+    if constexpr (PARTS == 3) {
+        if (packed) mxs_body<1, RT, WV>(acc, wt, xv, xs, 0, W.nb, w);
+        else mxs_body<3, RT, WV>(acc, wt, xv, xs, (int64_t)x.width * 2, W.nb, w);
+    } else {
+        mxs_body<PARTS, RT, WV>(acc, wt, xv, xs, 0, W.nb, w);
     }
 
 #pragma unroll
@@ -114,17 +153,19 @@ __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, Mx
         if (c >= t.rows) break;
         const int ln = ((r & 15) >> 2) * 16 + c, v = r & 3, n = o0 + r;
         float a = 0.f, u = 0.f;
+        const int np = packed ? 3 : 1;
+        for (int p = 0; p < np; p++)
 #pragma unroll
-        for (int k = 0; k < WV; k++) {
-            a += red[k][r >> 4][ln][v];
-            if (PAIR) u += red[k][RTM + (r >> 4)][ln][v];
-        }
+            for (int k = 0; k < WV; k++) {
+                a += red[k][r >> 4][ln + p * MXS_PACK][v];
+                if (PAIR) u += red[k][RTM + (r >> 4)][ln + p * MXS_PACK][v];
+            }
         const int pos = t.pos0 + c;
         if constexpr (PAIR) {
             if (n >= o.width) continue;
             uint8_t *dst = static_cast<uint8_t *>(o.y) + (int64_t)pos * o.ld;
             const float h = n < W.rows ? silu(a) * u : 0.0f;
-            if constexpr (P == 3) {
+            if constexpr (PARTS == 3) {
                 uint16_t p[3];
                 mx_split3(h, p);
 #pragma unroll
@@ -153,13 +194,31 @@ static hipError_t go(const MxMat &w, const MxMat &up, const MxX &x, const MxGrou
     return hipGetLastError();
 }
 
+// Waves per block: the chunks of a row, at most eight.
+template <int PARTS, int RT, bool PAIR>
+static hipError_t by_width(const MxMat &w, const MxMat &up, const MxX &x, const MxGroups &g,
+                           const MxOut &out, hipStream_t st) {
+    const int chunks = (w.nb + 15) / 16;
+    if (chunks <= 2) return go<PARTS, RT, 2, PAIR>(w, up, x, g, out, st);
+    if (chunks == 3 || chunks == 6) return go<PARTS, RT, 3, PAIR>(w, up, x, g, out, st);
+    if (chunks <= 4) return go<PARTS, RT, 4, PAIR>(w, up, x, g, out, st);
+    return go<PARTS, RT, 8, PAIR>(w, up, x, g, out, st);
+}
+
+template <int PARTS, bool PAIR>
+static hipError_t by_rows(const MxMat &w, const MxMat &up, const MxX &x, const MxGroups &g,
+                          const MxOut &out, hipStream_t st) {
+    if (g.n <= MXS_WIDE_ROWS) return by_width<PARTS, 2, PAIR>(w, up, x, g, out, st);
+    return by_width<PARTS, 4, PAIR>(w, up, x, g, out, st);
+}
+
 hipError_t launch_mx_stream(const MxMat &w, const MxMat &up, const MxX &x, int parts,
                             const MxGroups &g, const MxOut &out, hipStream_t st) {
-    if (up.q) return parts == 3 ? go<3, 2, 8, true>(w, up, x, g, out, st)
-                                : go<1, 2, 8, true>(w, up, x, g, out, st);
-    if (parts == 0) return go<0, 2, 4, false>(w, up, x, g, out, st);
-    if (parts == 1) return go<1, 2, 4, false>(w, up, x, g, out, st);
-    return go<3, 2, 4, false>(w, up, x, g, out, st);
+    if (up.q) return parts == 3 ? by_rows<3, true>(w, up, x, g, out, st)
+                                : by_rows<1, true>(w, up, x, g, out, st);
+    if (parts == 0) return by_rows<0, false>(w, up, x, g, out, st);
+    if (parts == 1) return by_rows<1, false>(w, up, x, g, out, st);
+    return by_rows<3, false>(w, up, x, g, out, st);
 }
 
 }  // namespace qmoe

@@ -28,32 +28,6 @@ constexpr int FP_WROWS = 256;
 // rows of a 128-bit read at one piece fall on 16 different bank quads.
 __device__ __forceinline__ int fp_slot(int m, int o) { return o ^ ((m >> 2) & 3); }
 
-// Scale bytes b0 .. b0 + 15 of a row of nb, 0 past its end (which stands for
-// 2^-127 and multiplies codes that are 0 there in x).
-__device__ __forceinline__ u32x4 fp_scales(const uint8_t *row, int b0, int nb) {
-    u32x4 v;
-    if (b0 + 16 <= nb) {
-        __builtin_memcpy(&v, row + b0, 16);
-    } else {
-        uint64_t part[2] = {0, 0};
-#pragma unroll 1
-        for (int j = 0; b0 + j < nb; j++) {
-            const uint64_t c = (uint64_t)row[b0 + j] << (8 * (j & 7));
-            if (j < 8) part[0] |= c;
-            else part[1] |= c;
-        }
-        __builtin_memcpy(&v, part, 16);
-    }
-    return v;
-}
-
-// Byte q of each dword: the scales of block q of four consecutive stages, the
-// byte of stage s at place s.
-__device__ __forceinline__ uint32_t fp_pick(u32x4 v, int q) {
-    const uint32_t sel = 0x0c0c0400u + 0x0101u * q;
-    return perm_b32(v[1], v[0], sel) | perm_b32(v[3], v[2], sel) << 16;
-}
-
 // x row (relative to `first`) of tile row m; rows past the tile and rows
 // without a row of x read one that exists.
 __device__ __forceinline__ int64_t fp_source(const MxGroups &g, const MxX &x, const MxTile &t, int m,
@@ -123,8 +97,8 @@ __device__ __forceinline__ void fp_mainloop(f32x16 (&acc)[XF][MXT_WF], const FpS
     };
     auto load_scales = [&](int it) {
 #pragma unroll
-        for (int j = 0; j < WF; j++) rws[j] = fp_scales(src.ws[j], 4 * it, nb);
-        rxs = fp_scales(src.xs, 4 * it, nb);
+        for (int j = 0; j < WF; j++) rws[j] = mx_scales16(src.ws[j], 4 * it, nb);
+        rxs = mx_scales16(src.xs, 4 * it, nb);
     };
     auto put_scales = [&](int half) {
         // every thread, rows again where there are fewer than threads: a branch
@@ -135,13 +109,13 @@ __device__ __forceinline__ void fp_mainloop(f32x16 (&acc)[XF][MXT_WF], const FpS
 #pragma unroll
         for (int h = 0; h < 2; h++) {
 #pragma unroll
-            for (int j = 0; j < WF; j++) sw[h][j] = fp_pick(rws[j], 2 * hh + h);
+            for (int j = 0; j < WF; j++) sw[h][j] = mx_pick(rws[j], 2 * hh + h);
         }
 #pragma unroll
         for (int i = 0; i < XC; i++) {
             const u32x4 v = ss[half * MXT_THREADS + 32 * i + l32];
-            sc[0][i] = fp_pick(v, 2 * hh);
-            sc[1][i] = fp_pick(v, 2 * hh + 1);
+            sc[0][i] = mx_pick(v, 2 * hh);
+            sc[1][i] = mx_pick(v, 2 * hh + 1);
         }
     };
     const int xp[2] = {fp_slot(l32, 2 * hh) * 16, fp_slot(l32, 2 * hh + 1) * 16};
