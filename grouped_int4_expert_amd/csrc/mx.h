@@ -128,73 +128,96 @@ struct MxTile {
     int e, pos0, rows, cb;
 };
 
-// The work item of this block: a tile of at most BM rows of one group and a
-// column block.  Every wave of the block runs it (no LDS): lane l sums the
-// tiles of its share of the experts, a scan over the wave finds the lane the
-// tile falls to, and that lane walks its experts.  Offsets are clamped to
-// [0, n], so no value of theirs leads outside the output.  The GPU hands
-// linear block ids to its 8 XCDs round-robin and each XCD has an L2 of its
-// own; each is given one contiguous run of the items, the column blocks of a
-// tile side by side.
-__device__ __forceinline__ bool mx_find(const MxGroups &g, int bm, int ncb, MxTile &t) {
-    const int lane = lane_id();
-    int total, mine = 0, before = 0, per = 0;
-    if (!g.offsets) {
-        total = (g.n + bm - 1) / bm;
-    } else {
-        per = (g.experts + QMOE_WAVE - 1) / QMOE_WAVE;
-        int last = 0;
-        for (int i = 0; i <= per; i++) {
-            const int e = min(lane * per + i, g.experts);
-            const int o = min(max(g.offsets[e], 0), g.n);
-            if (i > 0) mine += (max(o - last, 0) + bm - 1) / bm;
-            last = o;
-        }
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < QMOE_WAVE; o <<= 1) {
-            const int y = __shfl_up(inc, o, QMOE_WAVE);
-            if (lane >= o) inc += y;
-        }
-        before = inc - mine;
-        total = __builtin_amdgcn_readlane(inc, QMOE_WAVE - 1);
-    }
+// Inclusive sum over the lanes of a wave (DPP: within rows of 16 lanes, then
+// the row totals passed on).
+__device__ __forceinline__ int mx_wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31
+    return v;
+}
+
+// The work item of this block: a tile of at most bm rows of one group and a
+// column block.  Every wave of the block runs it (no LDS): lane l of round r
+// holds the offset of expert 64 r + l, all loads in flight at once, and a scan
+// over the lanes gives each expert's first tile.  Offsets are clamped to
+// [0, n], so no value of theirs leads outside the output.  The GPU hands linear
+// block ids to its 8 XCDs round-robin and each XCD has an L2 of its own; each
+// is given one contiguous run of the items.
+__device__ __forceinline__ bool mx_item(int total, int ncb, int64_t &item, int &tile) {
     const int64_t items = (int64_t)total * ncb;
     const int64_t per_xcd = (items + 7) / 8;
-    const int64_t w = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per_xcd || w >= items) return false;
-    const int tile = __builtin_amdgcn_readfirstlane((int)(w / ncb));
-    t.cb = __builtin_amdgcn_readfirstlane((int)(w - (int64_t)tile * ncb));
-    if (!g.offsets) {
-        t.e = 0;
-        t.pos0 = tile * bm;
-        t.rows = min(bm, g.n - t.pos0);
+    item = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per_xcd || item >= items) return false;
+    tile = (int)((uint64_t)item >> 32 ? item / ncb : (uint32_t)item / (uint32_t)ncb);
+    return true;
+}
+
+// Item `local` of a group of `rows` rows: the tiles of one column block side by
+// side, so that what they share of the weights is read from memory once.
+__device__ __forceinline__ void mx_place(MxTile &t, int first, int rows, int bm, int64_t local) {
+    const int tiles = (rows + bm - 1) / bm;
+    t.cb = (int)((uint64_t)local >> 32 ? local / tiles : (uint32_t)local / (uint32_t)tiles);
+    const int at = (int)(local - (int64_t)t.cb * tiles) * bm;
+    t.pos0 = first + at;
+    t.rows = min(bm, rows - at);
+}
+
+template <int ROUNDS>
+__device__ __forceinline__ bool mx_find_in(const MxGroups &g, int bm, int ncb, MxTile &t) {
+    const int lane = lane_id();
+    int o[ROUNDS + 1], last[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; r++)
+        o[r] = g.offsets[min(QMOE_WAVE * r + lane, g.experts)];
+    o[ROUNDS] = g.offsets[min(QMOE_WAVE * ROUNDS, g.experts)];
+    int total = 0;
+#pragma unroll
+    for (int r = 0; r < ROUNDS; r++) {
+        o[r] = min(max(o[r], 0), g.n);
+        int next = __shfl_down(o[r], 1, QMOE_WAVE);
+        const int after = min(max(__builtin_amdgcn_readfirstlane(o[r + 1]), 0), g.n);
+        if (lane == QMOE_WAVE - 1) next = after;
+        // inclusive number of tiles up to this expert
+        last[r] = total + mx_wave_scan((max(next - o[r], 0) + bm - 1) / bm);
+        total = __builtin_amdgcn_readlane(last[r], QMOE_WAVE - 1);
+    }
+    int64_t item;
+    int tile;
+    if (!mx_item(total, ncb, item, tile)) return false;
+    // the first expert whose tiles end behind `tile`
+#pragma unroll
+    for (int r = 0; r < ROUNDS; r++) {
+        const uint64_t behind = __ballot(last[r] > tile);
+        if (behind == 0) continue;
+        const int l = __ffsll((unsigned long long)behind) - 1;
+        const int first = __builtin_amdgcn_readlane(o[r], l);
+        const int end = l == QMOE_WAVE - 1 ? min(max(__builtin_amdgcn_readfirstlane(o[r + 1]), 0), g.n)
+                                           : __builtin_amdgcn_readlane(o[r], l + 1 & 63);
+        const int before = __builtin_amdgcn_readlane(last[r], l) - (max(end - first, 0) + bm - 1) / bm;
+        t.e = QMOE_WAVE * r + l;
+        mx_place(t, first, end - first, bm, item - (int64_t)before * ncb);
         return true;
     }
-    const bool here = tile >= before && tile < before + mine;
-    int e = 0, pos0 = 0, rows = 0;
-    if (here) {
-        int left = tile - before;
-        int last = min(max(g.offsets[min(lane * per, g.experts)], 0), g.n);
-        for (int i = 1; i <= per; i++) {
-            const int x = min(lane * per + i, g.experts);
-            const int o = min(max(g.offsets[x], 0), g.n);
-            const int c = max(o - last, 0);
-            const int nt = (c + bm - 1) / bm;
-            if (left >= 0 && left < nt) {
-                e = x - 1;
-                pos0 = last + left * bm;
-                rows = min(bm, c - left * bm);
-            }
-            left -= nt;
-            last = o;
-        }
+    return false;
+}
+
+__device__ __forceinline__ bool mx_find(const MxGroups &g, int bm, int ncb, MxTile &t) {
+    if (!g.offsets) {
+        int64_t item;
+        int tile;
+        if (!mx_item((g.n + bm - 1) / bm, ncb, item, tile)) return false;
+        t.e = 0;
+        mx_place(t, 0, g.n, bm, item);
+        return true;
     }
-    const int src = __ffsll((unsigned long long)__ballot(here)) - 1;
-    t.e = __builtin_amdgcn_readlane(e, src);
-    t.pos0 = __builtin_amdgcn_readlane(pos0, src);
-    t.rows = __builtin_amdgcn_readlane(rows, src);
-    return true;
+    if (g.experts <= QMOE_WAVE) return mx_find_in<1>(g, bm, ncb, t);
+    if (g.experts <= 2 * QMOE_WAVE) return mx_find_in<2>(g, bm, ncb, t);
+    if (g.experts <= 4 * QMOE_WAVE) return mx_find_in<4>(g, bm, ncb, t);
+    return mx_find_in<16>(g, bm, ncb, t);
 }
 
 // x row of output row `pos`; -1 where its pair names no row of x.

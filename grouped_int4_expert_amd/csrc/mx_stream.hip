@@ -1,5 +1,5 @@
 // MXFP4 products for few rows per matrix: the weights are streamed once per
-// pass of at most 16 rows.
+// pass of at most 16 rows (5 f32 rows).
 //
 // A block takes RT row tiles of 16 weight rows and one pass; its waves split
 // the inputs into chunks of 512 (wave w takes chunks w, w + WV, ...) and meet
@@ -24,22 +24,23 @@
 
 namespace qmoe {
 
-constexpr int MXS_ROWS = 16;    // rows per pass
+constexpr int MXS_PACK = 5;         // f32 rows whose parts share the 16 columns
+constexpr int mxs_rows(int parts) { return parts == 3 ? MXS_PACK : 16; }   // rows per pass
 constexpr int MXS_WIDE_ROWS = 32;   // up to here blocks take two tiles, above four
-constexpr int MXS_PACK = 5;     // f32 rows whose parts share the 16 columns
 
+// The weights of a block: bases of the matrix (or the pair) and the lane's row
+// offsets (one matrix stays below 2 GB).
 template <int RT>
 struct MxsWeights {
-    const uint8_t *q[RT], *s[RT];
+    const uint8_t *q[2], *s[2];
+    uint32_t qo[RT], so[RT];
 };
 
-// acc[i] += tile i of the weights times x over the wave's chunks.  NP parts of
-// x (`part` bytes apart) go into the same accumulators; 0: x is MXFP4.
-template <int NP, int RT, int WV>
+// acc[i] += tile i of the weights times x over the wave's chunks (MX: x is
+// MXFP4).
+template <bool MX, int RT, int RTM, int WV>
 __device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> &W,
-                                         const uint8_t *xv, const uint8_t *xs, int64_t part, int nb,
-                                         int w) {
-    constexpr int P = NP == 0 ? 1 : NP;
+                                         const uint8_t *xv, const uint8_t *xs, int nb, int w) {
     const int quarter = lane_id() >> 4;
     const int chunks = (nb + 15) / 16;
     for (int c = w; c < chunks; c += WV) {
@@ -47,20 +48,20 @@ __device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> 
         uint32_t cs[RT], xc = 0;
 #pragma unroll
         for (int i = 0; i < RT; i++) {
-            const u32x4 v = mx_scales16(W.s[i], 16 * c, nb);
+            const u32x4 v = mx_scales16(W.s[i / RTM] + W.so[i], 16 * c, nb);
 #pragma unroll
             for (int s = 0; s < 4; s++) {
                 // blocks past the row re-read its last: finite codes times zeros of x
                 const int b = min(16 * c + 4 * s + quarter, nb - 1);
-                cq[s][i] = *reinterpret_cast<const u32x4 *>(W.q[i] + (int64_t)b * 16);
+                cq[s][i] = *reinterpret_cast<const u32x4 *>(W.q[i / RTM] + (W.qo[i] + (uint32_t)b * 16));
             }
             cs[i] = mx_pick(v, quarter);
         }
-        if constexpr (NP == 0) xc = mx_pick(mx_scales16(xs, 16 * c, nb), quarter);
+        if constexpr (MX) xc = mx_pick(mx_scales16(xs, 16 * c, nb), quarter);
 #pragma unroll
         for (int s = 0; s < 4; s++) {
             const int b = 16 * c + 4 * s + quarter;
-            if constexpr (NP == 0) {
+            if constexpr (MX) {
                 u32x4 xq = *reinterpret_cast<const u32x4 *>(xv + (int64_t)min(b, nb - 1) * 16);
                 if (b >= nb) xq = u32x4{0, 0, 0, 0};
                 const i32x8 xb = {(int)xq[0], (int)xq[1], (int)xq[2], (int)xq[3], 0, 0, 0, 0};
@@ -79,21 +80,17 @@ __device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> 
                 // x rows hold zeros up to a whole step past their end; the steps
                 // after that are not computed
                 if (16 * c + 4 * s >= nb) break;
-                bf16x8 xf[P][4];
+                bf16x8 xf[4];
 #pragma unroll
-                for (int p = 0; p < P; p++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        xf[p][j] = *reinterpret_cast<const bf16x8 *>(xv + p * part + (int64_t)b * 64 + j * 16);
+                for (int j = 0; j < 4; j++)
+                    xf[j] = *reinterpret_cast<const bf16x8 *>(xv + (int64_t)b * 64 + j * 16);
 #pragma unroll
                 for (int i = 0; i < RT; i++) {
                     const float sc = mx_scale((cs[i] >> (8 * s)) & 255u);
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         const bf16x8 wf = __builtin_bit_cast(bf16x8, mx_decode8(cq[s][i][j], sc));
-#pragma unroll
-                        for (int p = 0; p < P; p++)
-                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[p][j], acc[i], 0, 0, 0);
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[j], acc[i], 0, 0, 0);
                     }
                 }
             }
@@ -110,38 +107,34 @@ __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, Mx
     __shared__ __attribute__((aligned(16))) float red[WV][RT][64][4];
     const int ncb = ((PAIR ? o.width : W.rows) + 16 * RTM - 1) / (16 * RTM);
     MxTile t;
-    if (!mx_find(g, MXS_ROWS, ncb, t)) return;
+    if (!mx_find(g, mxs_rows(PARTS), ncb, t)) return;
     const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
     const int r16 = lane & 15;
     const int o0 = t.cb * 16 * RTM;
 
-    // this lane's x row, and with packed parts its part
-    const bool packed = PARTS == 3 && t.rows <= MXS_PACK;
-    const int part = packed ? min(r16 / MXS_PACK, 2) : 0;
-    const int col = min(packed ? r16 % MXS_PACK : r16, t.rows - 1);
+    // this lane's x row, and of f32 rows its part
+    const int part = PARTS == 3 ? min(r16 / MXS_PACK, 2) : 0;
+    const int col = min(PARTS == 3 ? r16 % MXS_PACK : r16, t.rows - 1);
     const int64_t src = max(mx_source(g, x, t.pos0 + col), (int64_t)0);
     const uint8_t *xv = x.v + src * x.ld + (int64_t)part * x.width * 2;
     const uint8_t *xs = PARTS == 0 ? x.s + src * W.nb : nullptr;
 
     MxsWeights<RT> wt;
+    wt.q[0] = W.q + (int64_t)t.e * W.q_stride;
+    wt.s[0] = W.s + (int64_t)t.e * W.s_stride;
+    wt.q[1] = PAIR ? U.q + (int64_t)t.e * U.q_stride : nullptr;
+    wt.s[1] = PAIR ? U.s + (int64_t)t.e * U.s_stride : nullptr;
 #pragma unroll
     for (int i = 0; i < RT; i++) {
-        const bool second = PAIR && i >= RTM;
-        const MxMat &M = second ? U : W;
-        const int row = min(o0 + 16 * (i - (second ? RTM : 0)) + r16, M.rows - 1);
-        wt.q[i] = M.q + (int64_t)t.e * M.q_stride + (int64_t)row * M.nb * 16;
-        wt.s[i] = M.s + (int64_t)t.e * M.s_stride + (int64_t)row * M.nb;
+        const uint32_t row = (uint32_t)min(o0 + 16 * (i % RTM) + r16, W.rows - 1);
+        wt.qo[i] = row * (uint32_t)W.nb * 16;
+        wt.so[i] = row * (uint32_t)W.nb;
     }
 
     f32x4 acc[RT];
 #pragma unroll
     for (int i = 0; i < RT; i++) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if constexpr (PARTS == 3) {
-        if (packed) mxs_body<1, RT, WV>(acc, wt, xv, xs, 0, W.nb, w);
-        else mxs_body<3, RT, WV>(acc, wt, xv, xs, (int64_t)x.width * 2, W.nb, w);
-    } else {
-        mxs_body<PARTS, RT, WV>(acc, wt, xv, xs, 0, W.nb, w);
-    }
+    mxs_body<PARTS == 0, RT, RTM, WV>(acc, wt, xv, xs, W.nb, w);
 
 #pragma unroll
     for (int i = 0; i < RT; i++) *reinterpret_cast<f32x4 *>(red[w][i][lane]) = acc[i];
@@ -153,8 +146,8 @@ __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, Mx
         if (c >= t.rows) break;
         const int ln = ((r & 15) >> 2) * 16 + c, v = r & 3, n = o0 + r;
         float a = 0.f, u = 0.f;
-        const int np = packed ? 3 : 1;
-        for (int p = 0; p < np; p++)
+#pragma unroll
+        for (int p = 0; p < (PARTS == 3 ? 3 : 1); p++)
 #pragma unroll
             for (int k = 0; k < WV; k++) {
                 a += red[k][r >> 4][ln + p * MXS_PACK][v];
@@ -188,21 +181,32 @@ static hipError_t go(const MxMat &w, const MxMat &up, const MxX &x, const MxGrou
                      const MxOut &out, hipStream_t st) {
     constexpr int RTM = PAIR ? RT / 2 : RT;
     const int64_t ncb = ((PAIR ? out.width : w.rows) + 16 * RTM - 1) / (16 * RTM);
-    const dim3 grid(mx_grid(mx_max_tiles(g, MXS_ROWS) * ncb));
+    const dim3 grid(mx_grid(mx_max_tiles(g, mxs_rows(PARTS)) * ncb));
     hipLaunchKernelGGL((mx_stream_kernel<PARTS, RT, WV, PAIR>), grid, dim3(WV * 64), 0, st, w, up, x,
                        g, out);
     return hipGetLastError();
 }
 
-// Waves per block: the chunks of a row, at most eight.
+// Waves per block.  Calls of few rows (two tiles) split the inputs as far as
+// they go, for latency.  Larger ones want several blocks per CU, so that one's
+// loads run under another's start and end: four waves (bf16, 64 tokens of a
+// 128-expert projection: 8 waves 107 us, 4 waves 89, 2 waves 93, 1 wave 93), two
+// for f32 rows, whose passes hold fewer rows (64-token layer: gate+up 4 waves
+// 243 us, 2 waves 241; down 3 waves 134, 1 wave 118).
 template <int PARTS, int RT, bool PAIR>
 static hipError_t by_width(const MxMat &w, const MxMat &up, const MxX &x, const MxGroups &g,
                            const MxOut &out, hipStream_t st) {
     const int chunks = (w.nb + 15) / 16;
-    if (chunks <= 2) return go<PARTS, RT, 2, PAIR>(w, up, x, g, out, st);
-    if (chunks == 3 || chunks == 6) return go<PARTS, RT, 3, PAIR>(w, up, x, g, out, st);
-    if (chunks <= 4) return go<PARTS, RT, 4, PAIR>(w, up, x, g, out, st);
-    return go<PARTS, RT, 8, PAIR>(w, up, x, g, out, st);
+    if constexpr (RT == 4 && PARTS == 3) {
+        if (chunks <= 3) return go<PARTS, RT, 1, PAIR>(w, up, x, g, out, st);
+        return go<PARTS, RT, 2, PAIR>(w, up, x, g, out, st);
+    } else {
+        if (chunks == 1) return go<PARTS, RT, 1, PAIR>(w, up, x, g, out, st);
+        if (chunks == 2) return go<PARTS, RT, 2, PAIR>(w, up, x, g, out, st);
+        if (chunks == 3) return go<PARTS, RT, 3, PAIR>(w, up, x, g, out, st);
+        if (RT == 4 || chunks == 4) return go<PARTS, RT, 4, PAIR>(w, up, x, g, out, st);
+        return go<PARTS, RT, 8, PAIR>(w, up, x, g, out, st);
+    }
 }
 
 template <int PARTS, bool PAIR>
