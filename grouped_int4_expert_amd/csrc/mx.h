@@ -46,6 +46,17 @@ struct MxGroups {
     int k, experts, n;
 };
 
+// Rows of f32 or bf16 as a caller holds them (any stride, any alignment of the
+// element), with the routing of a layer call (ids [tokens][k]; nullptr: one
+// matrix).  rows: rows of x, or pairs with ids.
+struct MxFew {
+    const void *x;
+    int64_t ld;         // elements
+    int cols, width;    // width: cols padded to 128
+    const int32_t *ids;
+    int k, experts, rows;
+};
+
 // What a product writes.
 enum { MX_OUT_F32 = 0, MX_OUT_BF16 = 1 };
 struct MxOut {
@@ -118,6 +129,42 @@ __device__ __forceinline__ void mx_split3(float x, uint16_t p[3]) {
     p[0] = (uint16_t)(top >> 16);
     p[1] = (uint16_t)(m >> 16);
     p[2] = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
+// Eight elements of a row from column c on as f32, zero past `cols`.  Rows
+// may start at any element: a load at less than its size's alignment is one
+// instruction on this GPU all the same.
+template <bool F32>
+__device__ __forceinline__ void mx_load8(const void *x, int64_t at, int left, float v[8]) {
+    if (left >= 8) {
+        if (F32) {
+            f32x4 a, b;
+            const float *p = static_cast<const float *>(x) + at;
+            __builtin_memcpy(&a, p, 16);
+            __builtin_memcpy(&b, p + 4, 16);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[i] = a[i];
+                v[4 + i] = b[i];
+            }
+        } else {
+            u32x4 a;
+            __builtin_memcpy(&a, static_cast<const uint16_t *>(x) + at, 16);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = __uint_as_float(a[i] << 16);
+                v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        v[i] = 0.0f;
+        if (i < left)
+            v[i] = F32 ? static_cast<const float *>(x)[at + i]
+                       : __uint_as_float((uint32_t) static_cast<const uint16_t *>(x)[at + i] << 16);
+    }
 }
 
 __device__ __forceinline__ uint16_t mx_bf16(float x) {
@@ -248,6 +295,18 @@ hipError_t launch_mx_parts(const void *x, bool f32, int64_t rows, int cols, int6
 // silu(W x) * (up x) instead of y (out.y, out.ld, out.width).
 hipError_t launch_mx_stream(const MxMat &w, const MxMat &up, const MxX &x, int parts,
                             const MxGroups &g, const MxOut &out, hipStream_t st);
+// A decode step (mx_decode.hip): a matrix times rows that fit one block's LDS
+// (up.q == nullptr), h parts of every pair, and the weighted sum of a token's
+// down projections.
+constexpr int MXF_LDS = 80 * 1024;          // two blocks per CU
+constexpr int MXF_DOWN_LDS = 152 * 1024;
+bool mx_few_matmul_fits(int parts, int rows, int width);
+bool mx_few_layer_fits(int parts, int width, int h_width);
+hipError_t launch_mx_few(const MxMat &w, const MxMat &up, int parts, const MxFew &f,
+                         const MxOut &out, hipStream_t st);
+hipError_t launch_mx_few_down(const MxMat &d, int parts, const MxFew &f, const uint8_t *h,
+                              int64_t h_ld, int width, const float *topk_w, int tokens, void *out,
+                              hipStream_t st);
 hipError_t launch_mx_tile(const MxMat &w, const MxMat &up, const MxX &x, int parts,
                           const MxGroups &g, const MxOut &out, hipStream_t st);
 hipError_t launch_mx_tile_fp4(const MxMat &w, const MxX &x, const MxGroups &g, const MxOut &out,

@@ -154,16 +154,27 @@ int product_checks(const qmoe_mxmat *W, int experts, int32_t x_dtype, const void
 int run_product(const qmoe_mxmat *W, int32_t x_dtype, const void *x, const uint8_t *x_s,
                 int64_t x_rows, int64_t x_ld, const MxGroups &g, int32_t y_dtype, void *y,
                 int64_t y_ld, void *ws, hipStream_t st) {
-    MxX o;
-    hipError_t e = operand(x_dtype, x, x_s, x_rows, W->cols, x_ld, ws, o, st);
-    if (e != hipSuccess) return QMOE_ERR_HIP;
     MxOut out{};
     out.y = y;
     out.ld = y_ld;
     out.type = y_dtype == QMOE_F32 ? MX_OUT_F32 : MX_OUT_BF16;
     out.vec = W->rows % 4 == 0 && y_ld % 4 == 0;
+    if (!g.offsets && x_dtype != QMOE_MXFP4 &&
+        mx_few_matmul_fits(parts_of(x_dtype), g.n, pad128(W->cols)))
+        return status_of(launch_mx_few(to_mx(W), MxMat{}, parts_of(x_dtype),
+                                       MxFew{x, x_ld, W->cols, pad128(W->cols), nullptr, 1, 1, g.n},
+                                       out, st));
+    MxX o;
+    const hipError_t e = operand(x_dtype, x, x_s, x_rows, W->cols, x_ld, ws, o, st);
+    if (e != hipSuccess) return QMOE_ERR_HIP;
     return status_of(product(to_mx(W), MxMat{}, o, x_dtype, g, out, st));
 }
+
+// Layer calls of at most this many pairs run as two launches without a worklist
+// (mx_decode.hip), which read an expert once per pair.  128 experts 4096 / 1536,
+// top-8, replayed graphs: 1 token 31 us against 43 with the worklist, 4 tokens
+// 98 against 104, 6 tokens 139 against 118.
+constexpr int FEW_PAIRS = 32;
 
 struct MxLayerWs {
     Worklist wl;
@@ -328,6 +339,18 @@ int qmoe_mx_layer(const qmoe_mx_layer_desc *desc, int32_t x_dtype, const void *x
         if (overlaps_mat(out, xb, a, E) || overlaps_mat(ws, L.bytes, a, E)) return QMOE_ERR_ALIAS;
 
     const hipStream_t st = as_stream(stream);
+    const int P = parts_of(x_dtype);
+    if (n <= FEW_PAIRS && mx_few_layer_fits(P, pad128(H), pad128(F))) {
+        const MxFew f{x, H, H, pad128(H), topk_ids, k, E, (int)n};
+        MxOut h{};
+        h.y = L.h;
+        h.width = pad128(F);
+        h.ld = (int64_t)P * h.width * 2;
+        hipError_t e = launch_mx_few(to_mx(&desc->gate), to_mx(&desc->up), P, f, h, st);
+        if (e == hipSuccess)
+            e = launch_mx_few_down(to_mx(&desc->down), P, f, L.h, h.ld, h.width, topk_w, tokens, out, st);
+        return status_of(e);
+    }
     hipError_t e = launch_worklist(topk_ids, (int)n, k, E, L.wl, L.hist, st);
     MxX xo;
     if (e == hipSuccess) e = operand(x_dtype, x, nullptr, tokens, H, H, L.x, xo, st);

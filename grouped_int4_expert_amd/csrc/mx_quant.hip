@@ -19,42 +19,6 @@ struct FastDiv {
 
 constexpr int64_t MX_MAX_ITEMS = (int64_t)1 << 30;   // items of one launch (FastDiv takes n < 2^31)
 
-// Eight elements of a row from column c on as f32, zero past `cols`.  Rows
-// may start at any element: a load at less than its size's alignment is one
-// instruction on this GPU all the same.
-template <bool F32>
-__device__ __forceinline__ void load8(const void *x, int64_t at, int left, float v[8]) {
-    if (left >= 8) {
-        if (F32) {
-            f32x4 a, b;
-            const float *p = static_cast<const float *>(x) + at;
-            __builtin_memcpy(&a, p, 16);
-            __builtin_memcpy(&b, p + 4, 16);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-        } else {
-            u32x4 a;
-            __builtin_memcpy(&a, static_cast<const uint16_t *>(x) + at, 16);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                v[2 * i] = __uint_as_float(a[i] << 16);
-                v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        v[i] = 0.0f;
-        if (i < left)
-            v[i] = F32 ? static_cast<const float *>(x)[at + i]
-                       : __uint_as_float((uint32_t) static_cast<const uint16_t *>(x)[at + i] << 16);
-    }
-}
-
 // Four lanes per block of 32, eight elements each: the block's largest
 // magnitude by two exchanges inside a quad, E = exponent of it - 2 (so that
 // element lies in [4, 8)), codes by the rounding conversion (nearest, ties to
@@ -70,7 +34,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *__restrict
     for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < items; i += gridDim.x * 256u) {
         const uint32_t row = quads.div(i), c = (i - row * quads.d) * 8;
         float v[8];
-        load8<F32>(x, (int64_t)row * ld + c, cols - (int)c, v);
+        mx_load8<F32>(x, (int64_t)row * ld + c, cols - (int)c, v);
         uint32_t m = 0;   // the bits of a magnitude order like the value
 #pragma unroll
         for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
@@ -143,7 +107,7 @@ __global__ void __launch_bounds__(256) mx_parts_kernel(const void *__restrict__ 
     for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < items; i += gridDim.x * 256u) {
         const uint32_t row = octets.div(i), c = (i - row * octets.d) * 8;
         float v[8];
-        load8<F32>(x, (int64_t)row * ld + c, cols - (int)c, v);
+        mx_load8<F32>(x, (int64_t)row * ld + c, cols - (int)c, v);
         uint16_t o[P][8];
 #pragma unroll
         for (int j = 0; j < 8; j++) {
