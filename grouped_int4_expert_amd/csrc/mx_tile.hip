@@ -1,33 +1,54 @@
 // MXFP4 weights times bf16 parts, many rows per matrix (see mx_tile.h).
 //
-// A stage is 64 inputs of one part; with three parts (f32 rows) the loop runs
-// over the parts of a stage's inputs in turn, so the weights of a stage are
-// read from memory once and twice more from the caches.  A lane holds block
-// 2 g + lane / 32 of its weight rows; MFMA k-step s multiplies inputs 8 s ..
-// 8 s + 7 of both blocks of the stage, decoded to exact bf16 values.
+// A stage is 64 inputs of one part, a unit 128 inputs: two stages, of each part
+// in turn.  A lane holds block 2 g + lane / 32 of its weight rows in stage g;
+// MFMA k-step s multiplies inputs 8 s .. 8 s + 7 of both blocks, decoded to
+// exact bf16 values.  Codes are loaded a unit at a time, 16 rows x 64
+// consecutive bytes per instruction (half as many cache lines as 32 rows x 32
+// bytes), and exchanging 16-lane groups between two such loads gives the
+// operands of the unit's two stages; with three parts the codes stay in
+// registers for all of them.  Scale bytes come eight of a row at a time, two
+// units ahead.
 #include "mx_tile.h"
 
 namespace qmoe {
 
 // Descriptors of a wave's weight operands.
 struct MxtWeights {
-    __amdgpu_buffer_rsrc_t q[MXT_WF], s[MXT_WF];
+    __amdgpu_buffer_rsrc_t q[MXT_WF];
 };
+
+// Scale bytes b0 .. b0 + 7 of a row of nb, 0 past its end, moved down by `hh`
+// bytes: block 2 g + hh of each pair at byte 2 g.
+__device__ __forceinline__ u32x2 mxt_scales8(const uint8_t *row, int b0, int nb, int hh) {
+    uint64_t v = 0;
+    if (b0 + 8 <= nb) {
+        __builtin_memcpy(&v, row + b0, 8);
+    } else {
+#pragma unroll 1
+        for (int j = 0; b0 + j < nb; j++) v |= (uint64_t)row[b0 + j] << (8 * j);
+    }
+    v >>= 8 * hh;
+    return u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+}
 
 template <int TF, int PARTS, bool PAIR>
 __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat U, MxX x,
                                                                 MxGroups g, MxOut o) {
     constexpr int WF = MXT_WF;
     constexpr int WROWS = PAIR ? 128 : 256;      // weight rows of one matrix per block
-    constexpr int LOADS = TF + 2 * WF;           // loads of a wave per stage
+    constexpr int SPU = 2 * PARTS;               // stages per unit
+    // loads a wave surely issued after those of a stage and before it waits for it
+    constexpr int NEWER = 2 * TF + (PARTS == 1 ? 2 * WF : 0);
     constexpr int VALU = (16 + TF * WF - 1) / (TF * WF);   // vector instructions after each MFMA
+    // one array per stage: reads of a stage then do not wait for loads into another
     __shared__ __attribute__((aligned(1024))) uint8_t s0[TF * 4096], s1[TF * 4096], s2[TF * 4096],
         s3[TF * 4096];
     const int ncb = ((PAIR ? o.width : W.rows) + WROWS - 1) / WROWS;
     MxTile t;
     if (!mx_find(g, 32 * TF, ncb, t)) return;
     const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
-    const int hh = lane >> 5, l32 = lane & 31;
+    const int hh = lane >> 5, l32 = lane & 31, nb = W.nb;
     const int n0 = t.cb * WROWS + (PAIR ? 32 : 64) * w;
 
     // x: without a gather the tile's rows are consecutive and the descriptor
@@ -46,15 +67,20 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
         xoff[i] = (uint32_t)((src < 0 ? 0 : src) * x.ld + piece * 16);
     }
     MxtWeights wt;
-    uint32_t woff[WF], soff[WF];
+    uint32_t woff[WF][2];
+    const uint8_t *srow[WF];
+    // 16-lane group c of a code load holds block {0, 2, 1, 3}[c] of its rows: the
+    // exchange then leaves blocks 0 and 1 in one register, 2 and 3 in the other
+    const int wblock = (lane >> 5) | ((lane >> 4) & 1) << 1;
 #pragma unroll
     for (int j = 0; j < WF; j++) {
         const MxMat &M = PAIR && j == 1 ? U : W;
-        const int row = min(n0 + (PAIR ? 0 : 32 * j) + l32, M.rows - 1);
-        wt.q[j] = make_rsrc(M.q + (int64_t)t.e * M.q_stride, (int64_t)M.rows * M.nb * 16);
-        wt.s[j] = make_rsrc(M.s + (int64_t)t.e * M.s_stride, (int64_t)M.rows * M.nb);
-        woff[j] = (uint32_t)(row * M.nb * 16 + 16 * hh);
-        soff[j] = (uint32_t)(row * M.nb + hh);
+        const int row = n0 + (PAIR ? 0 : 32 * j);
+        wt.q[j] = make_rsrc(M.q + (int64_t)t.e * M.q_stride, (int64_t)M.rows * nb * 16);
+#pragma unroll
+        for (int a = 0; a < 2; a++)
+            woff[j][a] = (uint32_t)(min(row + 16 * a + (lane & 15), M.rows - 1) * nb * 16 + 16 * wblock);
+        srow[j] = M.s + (int64_t)t.e * M.s_stride + (int64_t)min(row + l32, M.rows - 1) * nb;
     }
 
     f32x16 acc[TF][WF];
@@ -65,39 +91,55 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.f;
 
-    const int groups = (W.nb + 1) / 2, iters = groups * PARTS;
-    // a lane whose block lies past the row multiplies finite codes with x's zeros
-    const bool odd_tail = (W.nb & 1) && hh;
-    u32x4 rq[4][WF];
-    uint32_t rs[4][WF];
-    u32x4 xf[2][TF], wf[2][WF];
+    const int groups = (nb + 1) / 2, units = (nb + 3) / 4;
+    u32x4 rq[2][WF][2], xf[2][TF], wf[2][WF];     // rq: by unit, weight operand, then stage of the unit
+    u32x2 raw[WF], sv[WF];
     float sc[WF];
-    // Loads of iteration `it` (clamped to the last) into ring slot `slot`.
-    auto issue = [&](int it, int slot, uint8_t *buf) {
-        const int ic = min(it, iters - 1);
-        const int gi = ic / PARTS, p = ic - gi * PARTS;
-        const int xs = gi * 128 + p * x.width * 2;
+    // Stage s (0 .. 2 SPU - 1) of the two units from u0 on: its inputs of x.
+    // Stages past the last read as zeros (their weights are finite: any codes,
+    // and scale bytes of 0, which stand for 2^-127).
+    auto issue_x = [&](int u0, int s, uint8_t *buf) {
+        const int u = u0 + s / SPU, p = s % SPU / 2, half = s & 1;
+        const bool in = 2 * u + half < groups;
 #pragma unroll
         for (int i = 0; i < TF; i++)
-            mxt_load_lds(xr, buf + (i * 4 + w) * 1024, xoff[i], xs);
-#pragma unroll
-        for (int j = 0; j < WF; j++) {
-            rq[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(wt.q[j], woff[j], gi * 32, 0);
-            rs[slot][j] = __builtin_amdgcn_raw_buffer_load_b8(wt.s[j], soff[j], gi * 2, 0);
-        }
+            mxt_load_lds(xr, buf + (i * 4 + w) * 1024,
+                         in ? xoff[i] + (uint32_t)(u * 256 + half * 128 + p * x.width * 2) : OOB_OFFSET, 0);
     };
-    auto operands = [&](int b, int it, int slot, const uint8_t *buf, int ks) {
-        if (ks == 0) {
-            const bool pad = it >= iters || (odd_tail && it >= iters - PARTS);
+    auto issue_w = [&](int u, int slot) {
 #pragma unroll
-            for (int j = 0; j < WF; j++) sc[j] = pad ? 1.0f : mx_scale(rs[slot][j] & 255u);
+        for (int j = 0; j < WF; j++)
+#pragma unroll
+            for (int a = 0; a < 2; a++)
+                rq[slot][j][a] = __builtin_amdgcn_raw_buffer_load_b128(wt.q[j], woff[j][a], min(u, units - 1) * 64, 0);
+    };
+    auto load_scales = [&](int u) {
+#pragma unroll
+        for (int j = 0; j < WF; j++) raw[j] = mxt_scales8(srow[j], 4 * u, nb, hh);
+    };
+    // Operands of k-step ks of stage s into buffer b.
+    auto operands = [&](int b, int s, const uint8_t *buf, int ks) {
+        const int slot = s / SPU, half = s & 1;
+        if (ks == 0) {
+            if (s % SPU == 0) {
+#pragma unroll
+                for (int j = 0; j < WF; j++)
+#pragma unroll
+                    for (int v = 0; v < 4; v++) {
+                        const auto e = __builtin_amdgcn_permlane16_swap(rq[slot][j][0][v],
+                                                                        rq[slot][j][1][v], false, false);
+                        rq[slot][j][0][v] = e[0];
+                        rq[slot][j][1][v] = e[1];
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < WF; j++) sc[j] = mx_scale((sv[j][slot] >> (16 * half)) & 255u);
         }
-        const uint32_t keep = it < iters ? ~0u : 0u;   // iterations past the last add zeros
 #pragma unroll
         for (int i = 0; i < TF; i++)
             xf[b][i] = *reinterpret_cast<const u32x4 *>(&buf[mxt_off(32 * i + l32, 4 * hh + ks)]);
 #pragma unroll
-        for (int j = 0; j < WF; j++) wf[b][j] = mx_decode8(rq[slot][j][ks] & keep, sc[j]);
+        for (int j = 0; j < WF; j++) wf[b][j] = mx_decode8(rq[slot][j][half][ks], sc[j]);
     };
     auto mfmas = [&](int b) {
 #pragma unroll
@@ -108,39 +150,54 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
                                                                    __builtin_bit_cast(bf16x8, xf[b][i]),
                                                                    acc[i][j], 0, 0, 0);
     };
-    // Iteration `it`: k-steps 0..2 read the next step's operands while their
-    // MFMAs run; before step 3, iteration it + 1 is synchronised (this wave's
-    // LDS reads are done, its own loads of it + 1 have landed: two newer
-    // iterations stay in flight; barrier), the loads of it + 4 go into the
-    // stage just read, and step 3 reads the first operands of it + 1.
-    auto step = [&](int it, int slot, uint8_t *cur, uint8_t *next) {
+    // Stage s of the loop body: k-steps 0..2 read the next step's operands while
+    // their MFMAs run; before step 3 the next stage is synchronised (this wave's
+    // LDS reads are done; its own loads of the next stage have landed when only
+    // those issued after them are outstanding; barrier), the loads of stage
+    // s + 4 go into the stage just read, and step 3 reads the next stage's
+    // first operands.  A unit's last stage frees its codes' registers for the
+    // unit after the next.
+    auto stage = [&](int u0, int s, uint8_t *cur, uint8_t *next) {
 #pragma unroll
         for (int ks = 0; ks < 3; ks++) {
-            operands((ks + 1) & 1, it, slot, cur, ks + 1);
+            operands((ks + 1) & 1, s, cur, ks + 1);
             mfmas(ks & 1);
             mxt_interleave<TF * WF, TF, VALU>();
         }
         MXT_WAIT_LDS();
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * LOADS));
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(NEWER));
         __builtin_amdgcn_s_barrier();
-        issue(it + 4, slot, cur);
-        operands(0, it + 1, (slot + 1) & 3, next, 0);
+        issue_x(u0, s + 4, cur);
+        if (s % SPU == SPU - 1) issue_w(u0 + s / SPU + 2, s / SPU);
+        if (s == 2 * SPU - 1) {
+#pragma unroll
+            for (int j = 0; j < WF; j++) sv[j] = raw[j];
+        }
+        operands(0, (s + 1) % (2 * SPU), next, 0);
         mfmas(1);
         mxt_interleave<TF * WF, TF, VALU>();
     };
-    issue(0, 0, s0);
-    issue(1, 1, s1);
-    issue(2, 2, s2);
-    // all three: the compiler may order a stage's loads among those of the others here
+    uint8_t *const ring[4] = {s0, s1, s2, s3};
+#pragma unroll
+    for (int s = 0; s < 4; s++) issue_x(0, s, ring[s]);
+    issue_w(0, 0);
+    issue_w(1, 1);
+    load_scales(0);
+#pragma unroll
+    for (int j = 0; j < WF; j++) sv[j] = raw[j];
+    // all four: the compiler may order a stage's loads among those of the others here
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __builtin_amdgcn_s_barrier();
-    issue(3, 3, s3);
-    operands(0, 0, 0, s0, 0);
-    for (int it = 0; it < iters; it += 4) {
-        step(it, 0, s0, s1);
-        step(it + 1, 1, s1, s2);
-        step(it + 2, 2, s2, s3);
-        step(it + 3, 3, s3, s0);
+    operands(0, 0, s0, 0);
+    for (int u0 = 0; u0 < units; u0 += 2) {
+        load_scales(u0 + 2);
+#pragma unroll
+        for (int s = 0; s < 2 * SPU; s += 4) {
+            stage(u0, s, s0, s1);
+            stage(u0, s + 1, s1, s2);
+            stage(u0, s + 2, s2, s3);
+            stage(u0, s + 3, s3, s0);
+        }
     }
     // no load may still be writing LDS when the block ends
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
