@@ -129,12 +129,12 @@ int product_checks(const qmoe_mxmat *W, int experts, int32_t x_dtype, const void
     if (!aligned16(x) || !aligned16(y) || !aligned4(offsets) || !aligned4(pairs)) return QMOE_ERR_ALIGN;
     if (x_dtype == QMOE_MXFP4 && !aligned16(x_s)) return QMOE_ERR_ALIGN;
     const int64_t nb = mx_blocks(W->cols);
-    // 32-bit offsets: a gather spans all rows of x, otherwise a tile's rows do
+    // 31-bit offsets: a gather spans all rows of x, otherwise a tile's rows do
     const bool dir = direct_rows(x_dtype, W->cols, x_ld);
     const int64_t row = x_dtype == QMOE_MXFP4 ? nb * 16
                         : dir                 ? x_ld * 2
                                               : (int64_t)parts_of(x_dtype) * pad128(W->cols) * 2;
-    if ((pairs ? x_rows : 128) * row >= LIM31) return QMOE_ERR_UNSUPPORTED;
+    if ((pairs ? x_rows : 256) * row >= LIM31) return QMOE_ERR_UNSUPPORTED;
     const int64_t xb = x_dtype == QMOE_MXFP4 ? x_rows * nb * 16
                                              : span(x_rows, W->cols, x_ld, elem_bytes(x_dtype));
     const int64_t xsb = x_dtype == QMOE_MXFP4 ? x_rows * nb : 0;
@@ -216,7 +216,7 @@ int check_mx_layer(const qmoe_mx_layer_desc *d) {
             return QMOE_ERR_SHAPE;
     }
     // the padded rows of h and the part rows of x stay within a tile's 32-bit offsets
-    if ((int64_t)128 * 3 * 2 * pad128(d->hidden > d->inter ? d->hidden : d->inter) >= LIM31)
+    if ((int64_t)256 * 3 * 2 * pad128(d->hidden > d->inter ? d->hidden : d->inter) >= LIM31)
         return QMOE_ERR_UNSUPPORTED;
     return QMOE_OK;
 }

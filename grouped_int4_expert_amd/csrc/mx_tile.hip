@@ -101,10 +101,12 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
     auto issue_x = [&](int u0, int s, uint8_t *buf) {
         const int u = u0 + s / SPU, p = s % SPU / 2, half = s & 1;
         const bool in = 2 * u + half < groups;
+        // row offsets are below 2^31: with the top bit set they are past the end
+        // whatever else the range check counts in
+        const uint32_t off = in ? 0 : OOB_OFFSET;
+        const int so = in ? u * 256 + half * 128 + p * x.width * 2 : 0;
 #pragma unroll
-        for (int i = 0; i < TF; i++)
-            mxt_load_lds(xr, buf + (i * 4 + w) * 1024,
-                         in ? xoff[i] + (uint32_t)(u * 256 + half * 128 + p * x.width * 2) : OOB_OFFSET, 0);
+        for (int i = 0; i < TF; i++) mxt_load_lds(xr, buf + (i * 4 + w) * 1024, xoff[i] | off, so);
     };
     auto issue_w = [&](int u, int slot) {
 #pragma unroll
