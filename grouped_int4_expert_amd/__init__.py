@@ -610,12 +610,13 @@ def _rows(t, name):
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in _MX_TYPES:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() == 1:
-        t = t[None]
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) == 1:
+        return t.data_ptr(), 1, shape[0]
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [rows, cols] with dense rows")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    return ctypes.c_void_p(t.data_ptr()), t.shape[0], max(ld, t.shape[1])
+    rows, cols = shape
+    return t.data_ptr(), rows, max(t.stride(0), cols) if rows > 1 else cols
 
 
 def _same_device(device, **tensors):
@@ -624,56 +625,25 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name} is on {t.device}, the weights or first operand on {device}")
 
 
-def qmoe_mx_quantize(x, q=None, s=None, stream=None):
-    """f32 or bf16 rows [rows, cols] (rows may be strided) -> MXFP4 codes
-    uint8 [rows, ceil(cols/32) * 16] and scale bytes uint8 [rows, ceil(cols/32)]."""
-    p, rows, ld = _rows(x, "x")
-    cols = x.shape[-1]
-    nb = (cols + 31) // 32
-    q = torch.empty(rows, nb * 16, dtype=torch.uint8, device=x.device) if q is None else q
-    s = torch.empty(rows, nb, dtype=torch.uint8, device=x.device) if s is None else s
-    _mx_pair(q, s, rows, cols, "q", "s")
-    _same_device(x.device, q=q, s=s)
-    with _on(x.device):
-        _check(load().qmoe_mx_quantize(p, _MX_TYPES[x.dtype], rows, cols, ld, _ptr(q), _ptr(s),
-                                       _stream(stream)), "qmoe_mx_quantize")
-    return q, s
-
-
-def qmoe_mx_dequantize(q, s, cols, dtype=torch.float32, out=None, stream=None):
-    """MXFP4 rows -> f32 or bf16 values [rows, cols]; `out` rows may be strided."""
-    rows = q.shape[0]
-    _mx_pair(q, s, rows, cols, "q", "s")
-    if out is None:
-        if dtype not in _MX_TYPES:
-            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-        out = torch.empty(rows, cols, dtype=dtype, device=q.device)
-    p, r, ld = _rows(out, "out")
-    if r != rows or out.shape[-1] != cols:
-        raise ValueError(f"out must be [{rows}, {cols}]")
-    _same_device(q.device, s=s, out=out)
-    with _on(q.device):
-        _check(load().qmoe_mx_dequantize(_ptr(q), _ptr(s), rows, cols, p, _MX_TYPES[out.dtype], ld,
-                                         _stream(stream)), "qmoe_mx_dequantize")
-    return out
-
-
-class _on:
-    """The device a call runs on, made current for its length where it is not
-    (launches and `current_stream` go by the current device)."""
-    __slots__ = ("index", "before")
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _mx_call(device, fn, what, stream, *args):
+    """Run fn(*args, stream) on `device`, made current for the call where it is
+    not (launches go by the current device), on `stream` or the device's
+    current one."""
+    index = device.index
+    before = torch.cuda.current_device()
+    if before != index:
+        torch.cuda.set_device(index)
+    try:
+        if stream is None:
+            st = torch._C._cuda_getCurrentRawStream(index)
+        else:
+            st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        status = fn(*args, st)
+    finally:
+        if before != index:
+            torch.cuda.set_device(before)
+    if status != QMOE_OK:
+        raise QmoeError(status, what)
 
 
 def _mx_pair(q, s, rows, cols, nq, ns):
@@ -681,9 +651,48 @@ def _mx_pair(q, s, rows, cols, nq, ns):
     nb = (cols + 31) // 32
     _dev(q, nq, torch.uint8)
     _dev(s, ns, torch.uint8)
-    if tuple(q.shape) != (rows, nb * 16) or tuple(s.shape) != (rows, nb):
+    if q.shape != (rows, nb * 16) or s.shape != (rows, nb):
         raise ValueError(f"{nq}, {ns} must be [{rows}, {nb * 16}] and [{rows}, {nb}] for {cols} columns, "
                          f"got {tuple(q.shape)} and {tuple(s.shape)}")
+
+
+def qmoe_mx_quantize(x, q=None, s=None, stream=None):
+    """f32 or bf16 rows [rows, cols] (rows may be strided) -> MXFP4 codes
+    uint8 [rows, ceil(cols/32) * 16] and scale bytes uint8 [rows, ceil(cols/32)]."""
+    p, rows, ld = _rows(x, "x")
+    cols = x.shape[-1]
+    nb = (cols + 31) // 32
+    device = x.device
+    given = q is not None or s is not None
+    q = torch.empty((rows, nb * 16), dtype=torch.uint8, device=device) if q is None else q
+    s = torch.empty((rows, nb), dtype=torch.uint8, device=device) if s is None else s
+    if given:
+        _mx_pair(q, s, rows, cols, "q", "s")
+        _same_device(device, q=q, s=s)
+    _mx_call(device, load().qmoe_mx_quantize, "qmoe_mx_quantize", stream, p, _MX_TYPES[x.dtype], rows,
+             cols, ld, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def qmoe_mx_dequantize(q, s, cols, dtype=torch.float32, out=None, stream=None):
+    """MXFP4 rows -> f32 or bf16 values [rows, cols]; `out` rows may be strided."""
+    rows = q.shape[0]
+    _mx_pair(q, s, rows, cols, "q", "s")
+    device = q.device
+    _same_device(device, s=s)
+    if out is None:
+        if dtype not in _MX_TYPES:
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        p, ld = out.data_ptr(), cols
+    else:
+        p, r, ld = _rows(out, "out")
+        if r != rows or out.shape[-1] != cols:
+            raise ValueError(f"out must be [{rows}, {cols}]")
+        _same_device(device, out=out)
+    _mx_call(device, load().qmoe_mx_dequantize, "qmoe_mx_dequantize", stream, q.data_ptr(), s.data_ptr(),
+             rows, cols, p, _MX_TYPES[out.dtype], ld)
+    return out
 
 
 class MxMat:
@@ -739,11 +748,12 @@ def _mx_operand(W, x, x_s):
     if x_s is not None:
         _mx_pair(x, x_s, x.shape[0], W.cols, "x", "x_s")
         _same_device(W.device, x=x, x_s=x_s)
-        return QMOE_MXFP4, _ptr(x), _ptr(x_s), x.shape[0], W.cols
+        return QMOE_MXFP4, x.data_ptr(), x_s.data_ptr(), x.shape[0], W.cols
     p, rows, ld = _rows(x, "x")
     if x.shape[-1] != W.cols:
         raise ValueError(f"x has {x.shape[-1]} columns, the matrix {W.cols}")
-    _same_device(W.device, x=x)
+    if x.device != W.device:
+        _same_device(W.device, x=x)
     return _MX_TYPES[x.dtype], p, None, rows, ld
 
 
@@ -753,14 +763,26 @@ def _mx_out(W, x, x_s, n, out, out_dtype):
             out_dtype = torch.float32 if x_s is not None else x.dtype
         if out_dtype not in _MX_TYPES:
             raise TypeError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-        out = torch.empty(n, W.rows, dtype=out_dtype, device=W.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
+        out = torch.empty((n, W.rows), dtype=out_dtype, device=W.device)
+        return out, out.data_ptr(), W.rows
+    if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     p, rows, ld = _rows(out, "out")
     if rows != n or out.shape[-1] != W.rows:
         raise ValueError(f"out must be [{n}, {W.rows}]")
     _same_device(W.device, out=out)
     return out, p, ld
+
+
+def _mx_workspace(nb, device, ws, stream):
+    """(tensor to keep, pointer, bytes) of a call's workspace."""
+    if nb == 0:
+        return None, None, 0
+    if ws is not None:
+        _dev(ws, "ws", torch.uint8)
+        _same_device(device, ws=ws)
+    ws = _workspace(nb, device, ws, stream)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def qmoe_mx_matmul(W: MxMat, x, x_s=None, out=None, out_dtype=None, ws=None, stream=None):
@@ -770,11 +792,9 @@ def qmoe_mx_matmul(W: MxMat, x, x_s=None, out=None, out_dtype=None, ws=None, str
     code, p, ps, rows, ld = _mx_operand(W, x, x_s)
     y, py, y_ld = _mx_out(W, x, x_s, rows, out, out_dtype)
     lib = load()
-    with _on(W.device):
-        nb = lib.qmoe_mx_workspace_bytes(W.ref, code, rows, ld)
-        ws = _workspace(nb, W.device, ws, stream) if nb else None
-        _check(lib.qmoe_mx_matmul(W.ref, code, p, ps, rows, ld, _MX_TYPES[y.dtype], py, y_ld,
-                                  _ptr(ws), nb, _stream(stream)), "qmoe_mx_matmul")
+    ws, pw, nw = _mx_workspace(lib.qmoe_mx_workspace_bytes(W.ref, code, rows, ld), W.device, ws, stream)
+    _mx_call(W.device, lib.qmoe_mx_matmul, "qmoe_mx_matmul", stream, W.ref, code, p, ps, rows, ld,
+             _MX_TYPES[y.dtype], py, y_ld, pw, nw)
     return y
 
 
@@ -788,19 +808,16 @@ def qmoe_mx_grouped(W: MxMat, x, offsets, pairs=None, k=1, x_s=None, out=None, o
     if offsets.numel() != W.experts + 1:
         raise ValueError(f"offsets must hold {W.experts + 1} values, got {offsets.numel()}")
     code, p, ps, rows, ld = _mx_operand(W, x, x_s)
-    n = rows
+    n, pp = rows, None
     if pairs is not None:
         _dev(pairs, "pairs", torch.int32)
-        n = pairs.numel()
+        n, pp = pairs.numel(), pairs.data_ptr()
     _same_device(W.device, offsets=offsets, pairs=pairs)
     y, py, y_ld = _mx_out(W, x, x_s, n, out, out_dtype)
     lib = load()
-    with _on(W.device):
-        nb = lib.qmoe_mx_workspace_bytes(W.ref, code, rows, ld)
-        ws = _workspace(nb, W.device, ws, stream) if nb else None
-        _check(lib.qmoe_mx_grouped(W.ref, W.experts, code, p, ps, rows, ld, _ptr(offsets),
-                                   _ptr(pairs), k, n, _MX_TYPES[y.dtype], py, y_ld, _ptr(ws), nb,
-                                   _stream(stream)), "qmoe_mx_grouped")
+    ws, pw, nw = _mx_workspace(lib.qmoe_mx_workspace_bytes(W.ref, code, rows, ld), W.device, ws, stream)
+    _mx_call(W.device, lib.qmoe_mx_grouped, "qmoe_mx_grouped", stream, W.ref, W.experts, code, p, ps, rows,
+             ld, offsets.data_ptr(), pp, k, n, _MX_TYPES[y.dtype], py, y_ld, pw, nw)
     return y
 
 
@@ -812,18 +829,19 @@ def qmoe_mx_layer(layer: MxLayer, x, topk_ids, topk_w, out=None, ws=None, stream
     _dev(topk_w, "topk_w", torch.float32)
     code = _dtype_code(x)
     T, k = topk_ids.shape
-    if tuple(x.shape) != (T, layer.hidden) or topk_w.shape != topk_ids.shape:
+    if x.shape != (T, layer.hidden) or topk_w.shape != topk_ids.shape:
         raise ValueError(f"x must be [{T}, {layer.hidden}] and topk_w [{T}, {k}], got "
                          f"{tuple(x.shape)} and {tuple(topk_w.shape)}")
+    _same_device(layer.device, x=x, topk_ids=topk_ids, topk_w=topk_w)
     if out is None:
         out = torch.empty_like(x)
-    elif _dev(out, "out", x.dtype).shape != x.shape:
-        raise ValueError(f"out must be {tuple(x.shape)}")
-    _same_device(layer.device, x=x, topk_ids=topk_ids, topk_w=topk_w, out=out)
+    else:
+        if _dev(out, "out", x.dtype).shape != x.shape:
+            raise ValueError(f"out must be {tuple(x.shape)}")
+        _same_device(layer.device, out=out)
     lib = load()
-    with _on(layer.device):
-        nb = lib.qmoe_mx_layer_workspace_bytes(layer.ref, T, k, code)
-        ws = _workspace(nb, layer.device, ws, stream)
-        _check(lib.qmoe_mx_layer(layer.ref, code, _ptr(x), T, _ptr(topk_ids), _ptr(topk_w), k,
-                                 _ptr(out), _ptr(ws), ws.numel(), _stream(stream)), "qmoe_mx_layer")
+    ws, pw, nw = _mx_workspace(lib.qmoe_mx_layer_workspace_bytes(layer.ref, T, k, code), layer.device, ws,
+                               stream)
+    _mx_call(layer.device, lib.qmoe_mx_layer, "qmoe_mx_layer", stream, layer.ref, code, x.data_ptr(), T,
+             topk_ids.data_ptr(), topk_w.data_ptr(), k, out.data_ptr(), pw, nw)
     return out
