@@ -89,15 +89,44 @@ hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, i
                            st);
 }
 
-// Which kernel a product takes: passes of 16 rows that stream the weights
-// while groups hold few rows, tiles on the matrix cores otherwise.
-constexpr int STREAM_ROWS = 16;
-bool few_rows(const MxGroups &g) { return g.n <= (int64_t)STREAM_ROWS * g.experts; }
+// Which kernel a product takes: passes that stream the weights (mx_stream.hip),
+// or tiles (mx_tile.hip, mx_tile_fp4.hip).  The stream's time grows with rows x
+// weights; a tile's with the inputs alone, as long as the tiles of a call fit
+// the GPU at once, and is then repeated.  The constants are one matrix of 4096 x
+// 4096, 16 to 1024 rows, each kernel alone (us):
+//   rows          16    64   128   256   512  1024
+//   f32  stream   17    38    67   114   219   419     tiles  60  84  189  192  193  198
+//   bf16 stream   8.6   12    20    35    67   130     tiles  31  36   51   51   55   56
+//   MXFP4 stream  6.2   9.1   15    26    47    91     tiles  22  24   28   28   29   31
+// and a layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 405 at
+// 64 tokens, 480 and 451 at 96; bf16 310 and 338 at 96, 412 and 380 at 200.
+struct TileCost {
+    int slots;      // blocks the GPU holds at once
+    double ns;      // of one block, per input
+};
+bool takes_tiles(const MxGroups &g, int parts, int64_t rows, int64_t col_blocks, int64_t cols) {
+    static const double stream[3] = {5.3e-6, 7.5e-6, 24.4e-6};       // ns per row, weight row and input
+    static const TileCost cost[3][3] = {{{512, 5.9}, {512, 5.9}, {256, 6.8}},
+                                        {{1024, 7.6}, {512, 8.7}, {512, 12.5}},
+                                        {{768, 15.0}, {512, 20.0}, {512, 47.0}}};
+    const int type = parts == 3 ? 2 : parts;
+    const int64_t groups = g.offsets ? (g.n < g.experts ? g.n : g.experts) : 1;
+    const int64_t per = (g.n + groups - 1) / groups;
+    const int size = per <= 32 ? 0 : per <= 64 ? 1 : 2;
+    const int64_t tile = parts == 0 ? (size < 2 ? 64 : g.offsets ? 256 : 128) : 32 << size;
+    const int64_t blocks = groups * ((per + tile - 1) / tile) * col_blocks;
+    const TileCost c = cost[type][size];
+    const double tiles_ns = (double)((blocks + c.slots - 1) / c.slots) * c.ns * cols;
+    return stream[type] * g.n * rows * cols > tiles_ns;
+}
 
 hipError_t product(const MxMat &w, const MxMat &up, const MxX &x, int dtype, const MxGroups &g,
                    const MxOut &o, hipStream_t st) {
     const int parts = dtype == QMOE_MXFP4 ? 0 : parts_of(dtype);
-    if (few_rows(g)) return launch_mx_stream(w, up, x, parts, g, o, st);
+    const int64_t rows = up.q ? 2 * (int64_t)w.rows : w.rows;
+    const int64_t col_blocks = (rows + 255) / 256;
+    if (!takes_tiles(g, parts, rows, col_blocks, (int64_t)w.nb * MX_BLOCK))
+        return launch_mx_stream(w, up, x, parts, g, o, st);
     if (parts == 0) return launch_mx_tile_fp4(w, x, g, o, st);
     return launch_mx_tile(w, up, x, parts, g, o, st);
 }

@@ -91,24 +91,24 @@ def layer(gate, up, down, x, ids, w, parts, bf16):
     weight and the k additions, and out's own rounding."""
     T, H = x.shape
     F = gate.shape[1]
-    out, bound = np.zeros((T, H)), np.zeros((T, H))
-    top = np.zeros((T, H))
-    for t in range(T):
-        for j in range(ids.shape[1]):
-            e = int(ids[t, j])
-            if not 0 <= e < gate.shape[0]:
-                continue
-            a, am = product(gate[e], x[t:t + 1])
-            u, um = product(up[e], x[t:t + 1])
-            da, du = sum_bound(H, parts) * am, sum_bound(H, parts) * um
-            h = silu(a) * u
-            dh = 1.1 * da * np.abs(u) + np.abs(silu(a)) * du + 1.1 * da * du + 16 * U * np.abs(h)
-            if bf16:
-                dh = dh + UB * (np.abs(h) + dh)
-            y, ym = product(down[e], h)
-            dy = dh @ np.abs(down[e]).T + sum_bound(F, parts) * (ym + dh @ np.abs(down[e]).T)
-            out[t] += w[t, j] * y[0]
-            bound[t] += abs(w[t, j]) * (dy[0] + 2 * U * np.abs(y[0]))
-            top[t] += abs(w[t, j]) * (np.abs(y[0]) + dy[0])
+    out, bound, top = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
+    for e in range(gate.shape[0]):
+        t, j = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        a, am = product(gate[e], x[t])
+        u, um = product(up[e], x[t])
+        da, du = sum_bound(H, parts) * am, sum_bound(H, parts) * um
+        h = silu(a) * u
+        dh = 1.1 * da * np.abs(u) + np.abs(silu(a)) * du + 1.1 * da * du + 16 * U * np.abs(h)
+        if bf16:
+            dh = dh + UB * (np.abs(h) + dh)
+        y, ym = product(down[e], h)
+        far = dh @ np.abs(down[e]).T
+        dy = far + sum_bound(F, parts) * (ym + far)
+        wt = w[t, j][:, None]
+        np.add.at(out, t, wt * y)
+        np.add.at(bound, t, np.abs(wt) * (dy + 2 * U * np.abs(y)))
+        np.add.at(top, t, np.abs(wt) * (np.abs(y) + dy))
     bound += 2 * U * ids.shape[1] * top
     return out, bound + (UB if bf16 else U) * (np.abs(out) + bound)

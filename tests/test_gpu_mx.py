@@ -139,6 +139,52 @@ def test_matmul(kind, out, batch, rows, cols):
     check(y, want, ref.sum_bound(cols, parts(kind)) * m, TYPES[out], "matmul")
 
 
+# Products large enough for the tiles' kernels (rows x outputs counts, not inputs): whole and partial
+# tiles, odd widths on every side.
+@pytest.mark.parametrize("batch,rows,cols", [(2100, 1000, 64), (2049, 1021, 257), (1300, 2304, 96), (3001, 900, 33),
+                                             (1030, 3000, 1001)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_tiles(kind, out, batch, rows, cols):
+    test_matmul(kind, out, batch, rows, cols)
+
+
+@pytest.mark.parametrize("per", [20, 50, 150, 400])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_tiles(kind, gather, per):
+    """Ragged groups of `per` rows on average, one of them empty, for each size of tile."""
+    say(f"mx grouped tiles {kind} per={per} gather={gather}")
+    g = gen(per + gather)
+    experts, rows, cols = (70, 1300, 160) if per < 100 else (9, 2060, 321)
+    c = torch.randint(per // 2, per * 3 // 2, (experts,), generator=g)
+    c[3] = 0
+    used = int(c.sum())
+    n = used + 3
+    offsets = torch.zeros(experts + 1, dtype=torch.int32)
+    offsets[1:] = c.cumsum(0).to(torch.int32)
+    q, s = ref.rand_mx(g, (experts, rows), cols)
+    tokens = n // 2 + 1
+    x, x_s, xv = rows_of(kind, g, tokens if gather else n, cols)
+    pairs = torch.randint(0, tokens * 2, (n,), generator=g).to(torch.int32) if gather else None
+    if gather:
+        pairs[5] = -1
+    out = torch.full((n, rows), 9.0, device=DEV)
+    qm.qmoe_mx_grouped(qm.MxMat(q.to(DEV), s.to(DEV), cols), x, offsets.to(DEV),
+                       pairs=None if pairs is None else pairs.to(DEV), k=2 if gather else 1, x_s=x_s, out=out)
+    src = pairs.numpy() // 2 if gather else np.arange(n)
+    want, m = np.zeros((used, rows)), np.zeros((used, rows))
+    for e in range(experts):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if b > a:
+            want[a:b], m[a:b] = ref.product(ref.decode(q[e], s[e], cols), xv[src[a:b]])
+    if gather:
+        assert (out[5] == 0).all()
+        want[5] = 0
+    check(out[:used], want, ref.sum_bound(cols, parts(kind)) * m, torch.float32, "grouped tiles")
+    assert (out[used:] == 9.0).all()
+
+
 def group_sizes(kind, experts, g):
     if kind == "few":
         c = torch.randint(0, 4, (experts,), generator=g)
@@ -294,6 +340,12 @@ def test_layer(kind, T, E, H, F, k):
     assert got.dtype == x.dtype
     check_layer(got, want, bound, kind, "layer")
     assert torch.equal(got, qm.qmoe_mx_layer(dev, x.to(DEV), ids.to(DEV), w.to(DEV)))
+
+
+@pytest.mark.parametrize("T,E,H,F,k", [(700, 6, 1030, 420, 4), (900, 40, 512, 610, 2), (2500, 5, 384, 333, 1)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_layer_tiles(kind, T, E, H, F, k):
+    test_layer(kind, T, E, H, F, k)
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
