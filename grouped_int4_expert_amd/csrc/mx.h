@@ -66,7 +66,7 @@ struct MxOut {
     const float *w;     // row r is multiplied by w[wpairs[r]] (nullptr: no weights)
     const int32_t *wpairs;
     int width;          // h: padded width of a part
-    int vec;            // four consecutive outputs of a row may be stored at once
+    int vec;            // rows of y consist of whole, aligned 16-byte pieces
 };
 
 __device__ __forceinline__ float mx_scale(uint32_t c) {

@@ -1,5 +1,7 @@
 // C ABI of the MXFP4 entry points: checks, workspace layout and launch
 // sequencing.  As in abi.hip every check runs before the first HIP call.
+#include <algorithm>
+
 #include "abi_util.h"
 #include "launch.h"
 #include "mx.h"
@@ -91,24 +93,32 @@ hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, i
 
 // Which kernel a product takes: passes that stream the weights (mx_stream.hip),
 // or tiles (mx_tile.hip, mx_tile_fp4.hip).  The stream's time grows with rows x
-// weights; a tile's with the inputs alone, as long as the tiles of a call fit
-// the GPU at once, and is then repeated.  The constants are one matrix of 4096 x
-// 4096, 16 to 1024 rows, each kernel alone (us):
+// weights (every group's last pass half empty); a tile's with the inputs alone,
+// as long as the tiles of a call fit the GPU at once, and is then repeated; both
+// have to read the weights, which the stream does faster.  Measured: one matrix
+// of 4096 x 4096, 16 to 1024 rows, each kernel alone (us):
 //   rows          16    64   128   256   512  1024
 //   f32  stream   17    38    67   114   219   419     tiles  60  84  189  192  193  198
 //   bf16 stream   8.6   12    20    35    67   130     tiles  31  36   51   51   55   56
 //   MXFP4 stream  6.2   9.1   15    26    47    91     tiles  22  24   28   28   29   31
-// and a layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 405 at
+// The times over 512 to 8192 inputs of calls whose blocks fit at once give each
+// block's start and its time per input, below.  8 MXFP4 groups of 96 and 200 rows,
+// 2048 x 2048: stream 21 and 42 us, tiles 19 and 26; 1024 inputs: 12 and 24, 14 and
+// 20.  A layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 405 at
 // 64 tokens, 480 and 451 at 96; bf16 310 and 338 at 96, 412 and 380 at 200.
 struct TileCost {
-    int slots;      // blocks the GPU holds at once
-    double ns;      // of one block, per input
+    int slots;          // blocks the GPU holds at once
+    double start, ns;   // of one block: ns at its start and end, and per input
 };
 bool takes_tiles(const MxGroups &g, int parts, int64_t rows, int64_t col_blocks, int64_t cols) {
-    static const double stream[3] = {5.3e-6, 7.5e-6, 24.4e-6};       // ns per row, weight row and input
-    static const TileCost cost[3][3] = {{{512, 5.9}, {512, 5.9}, {256, 6.8}},
-                                        {{1024, 7.6}, {512, 8.7}, {512, 12.5}},
-                                        {{768, 15.0}, {512, 20.0}, {512, 47.0}}};
+    static const double stream[3] = {5.3e-6, 7.5e-6, 24.4e-6};   // ns per row, weight row and input
+    static const double bytes_per_ns[3] = {3000, 3600, 3100};    // weights through the tiles; streamed:
+    const double streamed_per_ns = 4600, stream_start = 4000;
+    static const int pass[3] = {16, 16, 5};
+    static const TileCost cost[3][3] = {        // tiles of 32, 64, 128 rows; MXFP4: 64, 64, 128 (256 in groups)
+        {{512, 6300, 4.2}, {512, 6300, 4.2}, {256, 9400, 4.9}},
+        {{1024, 4200, 6.5}, {512, 5400, 7.4}, {512, 7700, 11.0}},
+        {{768, 4800, 12.7}, {512, 5500, 19.2}, {512, 7800, 41.1}}};
     const int type = parts == 3 ? 2 : parts;
     const int64_t groups = g.offsets ? (g.n < g.experts ? g.n : g.experts) : 1;
     const int64_t per = (g.n + groups - 1) / groups;
@@ -116,8 +126,12 @@ bool takes_tiles(const MxGroups &g, int parts, int64_t rows, int64_t col_blocks,
     const int64_t tile = parts == 0 ? (size < 2 ? 64 : g.offsets ? 256 : 128) : 32 << size;
     const int64_t blocks = groups * ((per + tile - 1) / tile) * col_blocks;
     const TileCost c = cost[type][size];
-    const double tiles_ns = (double)((blocks + c.slots - 1) / c.slots) * c.ns * cols;
-    return stream[type] * g.n * rows * cols > tiles_ns;
+    const double bytes = (double)groups * rows * cols * 17 / 32;
+    const double tiles_ns = std::max((double)((blocks + c.slots - 1) / c.slots) * (c.start + c.ns * cols),
+                                     bytes / bytes_per_ns[type]);
+    const double stream_ns = stream_start + std::max(stream[type] * (g.n + groups * pass[type] / 2) * rows * cols,
+                                                       bytes / streamed_per_ns);
+    return stream_ns > tiles_ns;
 }
 
 hipError_t product(const MxMat &w, const MxMat &up, const MxX &x, int dtype, const MxGroups &g,
@@ -187,7 +201,8 @@ int run_product(const qmoe_mxmat *W, int32_t x_dtype, const void *x, const uint8
     out.y = y;
     out.ld = y_ld;
     out.type = y_dtype == QMOE_F32 ? MX_OUT_F32 : MX_OUT_BF16;
-    out.vec = W->rows % 4 == 0 && y_ld % 4 == 0;
+    const int wide = y_dtype == QMOE_F32 ? 4 : 8;      // outputs of a 16-byte store
+    out.vec = W->rows % wide == 0 && y_ld % wide == 0;
     if (!g.offsets && x_dtype != QMOE_MXFP4 &&
         mx_few_matmul_fits(parts_of(x_dtype), g.n, pad128(W->cols)))
         return status_of(launch_mx_few(to_mx(W), MxMat{}, parts_of(x_dtype),

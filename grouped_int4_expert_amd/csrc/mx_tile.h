@@ -52,16 +52,8 @@ __device__ __forceinline__ void mxt_interleave() {
 __device__ __forceinline__ void mxt_put4(const MxOut &o, int64_t pos, int n, int rows,
                                          const float v[4]) {
     const int64_t at = pos * o.ld + n;
-    if (o.vec) {
-        if (n >= rows) return;               // rows is a multiple of 4 here
-        if (o.type == MX_OUT_F32) {
-            __builtin_memcpy(__builtin_assume_aligned(static_cast<float *>(o.y) + at, 16), v, 16);
-        } else {
-            uint16_t b[4];
-#pragma unroll
-            for (int r = 0; r < 4; r++) b[r] = mx_bf16(v[r]);
-            __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t *>(o.y) + at, 8), b, 8);
-        }
+    if (o.type == MX_OUT_F32 && o.vec) {
+        if (n < rows) __builtin_memcpy(__builtin_assume_aligned(static_cast<float *>(o.y) + at, 16), v, 16);
         return;
     }
 #pragma unroll
@@ -70,6 +62,19 @@ __device__ __forceinline__ void mxt_put4(const MxOut &o, int64_t pos, int n, int
         if (o.type == MX_OUT_F32) static_cast<float *>(o.y)[at + r] = v[r];
         else static_cast<uint16_t *>(o.y)[at + r] = mx_bf16(v[r]);
     }
+}
+
+// 16-bit results: the two lanes that share a row of y exchange, so that each
+// holds eight consecutive outputs of it and stores 16 bytes: of outputs 16 p ..
+// 16 p + 15 lane / 32 = 0 the lower eight, 1 the upper.  `a` and `b` are a lane's
+// four at 16 p + 4 (lane / 32) and at 16 p + 8 + 4 (lane / 32).
+__device__ __forceinline__ u32x4 mxt_eight(const uint16_t a[4], const uint16_t b[4]) {
+    u32x2 u, v;
+    __builtin_memcpy(&u, a, 8);
+    __builtin_memcpy(&v, b, 8);
+    const auto lo = __builtin_amdgcn_permlane32_swap(u[0], v[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap(u[1], v[1], false, false);
+    return u32x4{lo[0], hi[0], lo[1], hi[1]};
 }
 
 // Writes the accumulators of a wave.  acc[i][j][4 q + r]: x row 32 i +
@@ -88,27 +93,32 @@ __device__ __forceinline__ void mxt_store(const f32x16 (&acc)[TF][MXT_WF], const
             // operand 0: gate rows n0 .., operand 1: the same rows of up
             uint16_t *dst = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(o.y) + pos * o.ld);
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int n = n0 + 8 * q + 4 * hh;
-                if (n >= o.width) continue;        // o.width is a multiple of 4
-                uint16_t p[PARTS][4];
+            for (int p2 = 0; p2 < 2; p2++) {
+                uint16_t p[PARTS][2][4];
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const float a = acc[i][0][4 * q + r], u = acc[i][1][4 * q + r];
-                    const bool in = n + r < rows_w;     // the padding of a part is zero
-                    if constexpr (PARTS == 3) {
-                        uint16_t s[3];
-                        mx_split3(in ? silu(a) * u : 0.0f, s);
+                for (int d = 0; d < 2; d++)
 #pragma unroll
-                        for (int k = 0; k < 3; k++) p[k][r] = s[k];
-                    } else {
-                        // h is rounded to bf16, x's own type
-                        p[0][r] = mx_bf16(in ? silu_fast(a) * u : 0.0f);
+                    for (int r = 0; r < 4; r++) {
+                        const int v = 8 * p2 + 4 * d + r;
+                        const float a = acc[i][0][v], u = acc[i][1][v];
+                        // the padding of a part is zero
+                        const bool in = n0 + 16 * p2 + 8 * d + 4 * hh + r < rows_w;
+                        if constexpr (PARTS == 3) {
+                            uint16_t s[3];
+                            mx_split3(in ? silu(a) * u : 0.0f, s);
+#pragma unroll
+                            for (int k = 0; k < 3; k++) p[k][d][r] = s[k];
+                        } else {
+                            // h is rounded to bf16, x's own type
+                            p[0][d][r] = mx_bf16(in ? silu_fast(a) * u : 0.0f);
+                        }
                     }
-                }
+                const int n = n0 + 16 * p2 + 8 * hh;      // o.width is a multiple of 8
 #pragma unroll
-                for (int k = 0; k < PARTS; k++)
-                    __builtin_memcpy(__builtin_assume_aligned(dst + k * o.width + n, 8), p[k], 8);
+                for (int k = 0; k < PARTS; k++) {
+                    const u32x4 e = mxt_eight(p[k][0], p[k][1]);
+                    if (n < o.width) *reinterpret_cast<u32x4 *>(dst + k * o.width + n) = e;
+                }
             }
         } else {
             float f = 1.0f;
@@ -117,13 +127,27 @@ __device__ __forceinline__ void mxt_store(const f32x16 (&acc)[TF][MXT_WF], const
             else none = mx_source(g, x, (int)pos) < 0;
 #pragma unroll
             for (int j = 0; j < MXT_WF; j++) {
+                if (o.type == MX_OUT_BF16 && o.vec) {
+#pragma unroll
+                    for (int p2 = 0; p2 < 2; p2++) {
+                        uint16_t p[2][4];
+#pragma unroll
+                        for (int d = 0; d < 2; d++)
+#pragma unroll
+                            for (int r = 0; r < 4; r++)
+                                p[d][r] = mx_bf16(none ? 0.0f : acc[i][j][8 * p2 + 4 * d + r] * f);
+                        const u32x4 e = mxt_eight(p[0], p[1]);
+                        const int n = n0 + 32 * j + 16 * p2 + 8 * hh;
+                        if (n < rows_w) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(o.y) + pos * o.ld + n) = e;
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    const int n = n0 + 32 * j + 8 * q + 4 * hh;
                     float v[4];
 #pragma unroll
                     for (int r = 0; r < 4; r++) v[r] = none ? 0.0f : acc[i][j][4 * q + r] * f;
-                    mxt_put4(o, pos, n, rows_w, v);
+                    mxt_put4(o, pos, n0 + 32 * j + 8 * q + 4 * hh, rows_w, v);
                 }
             }
         }

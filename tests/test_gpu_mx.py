@@ -413,3 +413,138 @@ def test_quantize_route_group_and_layer_together(T):
     a4 = qm.qmoe_mx_grouped(mats[0], xq, wl["offsets"], pairs=wl["pairs"], k=k, x_s=xs)
     av = qm.qmoe_mx_grouped(mats[0], qm.qmoe_mx_dequantize(xq, xs, H), wl["offsets"], pairs=wl["pairs"], k=k)
     assert float((a4 - av).norm() / av.norm()) <= 2.0 ** -20
+
+
+# ------------------------------------------------- streams, graphs, large stacks
+
+def calls(T, seed=77, E=12, H=384, F=224, k=3):
+    """Every entry point once on one set of inputs: a list of functions without arguments."""
+    g = gen(seed + T)
+    layer, _ = make_layer(g, E, H, F)
+    x = torch.randn(T, H, generator=g)
+    ids, w = routing(g, T, E, k)
+    xd, xb, ids, w = x.to(DEV), x.bfloat16().to(DEV), ids.to(DEV), w.to(DEV)
+    wl = qm.qmoe_worklist(ids, E)
+    q, s = qm.qmoe_mx_quantize(xd)
+    one = qm.MxMat(layer.gate.q[1], layer.gate.s[1], H)
+    st = {}
+    return [lambda **kw: qm.qmoe_mx_quantize(xb, **kw)[0],
+            lambda **kw: qm.qmoe_mx_dequantize(q, s, H, **kw),
+            lambda **kw: qm.qmoe_mx_matmul(one, xd, **kw),
+            lambda **kw: qm.qmoe_mx_matmul(one, q, x_s=s, **kw),
+            lambda **kw: qm.qmoe_mx_grouped(layer.up, xd, wl["offsets"], pairs=wl["pairs"], k=k, **kw),
+            lambda **kw: qm.qmoe_mx_grouped(layer.up, xb, wl["offsets"], pairs=wl["pairs"], k=k, **kw),
+            lambda **kw: qm.qmoe_mx_grouped(layer.up, q, wl["offsets"], pairs=wl["pairs"], k=k, x_s=s, **kw),
+            lambda **kw: qm.qmoe_mx_layer(layer, xd, ids, w, **kw),
+            lambda **kw: qm.qmoe_mx_layer(layer, xb, ids, w, **kw)], (xd, xb, st)
+
+
+@pytest.mark.parametrize("T", [1, 7, 60, 3000])
+def test_replayed_graphs(T):
+    """Two captured graphs of the same calls (each with workspaces of its own), replayed in turn with eager
+    work between: every replay gives the eager results of the inputs as they are then."""
+    say(f"mx graphs T={T}")
+    fs, (xd, xb, _) = calls(T)
+    for f in fs:
+        f()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs = [f() for f in fs]
+        graphs.append((gr, outs))
+    for r in range(4):
+        xd.mul_(1.25)
+        xb.mul_(-1.0)
+        want = [f() for f in fs]
+        gr, outs = graphs[r & 1]
+        for o in outs:
+            o.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs, want)):
+            assert torch.equal(a, b), (T, r, i)
+
+
+@pytest.mark.parametrize("T", [2, 90])
+def test_streams(T):
+    """Calls on two streams at once, each given by argument, equal the same calls on the current one."""
+    say(f"mx streams T={T}")
+    fs, keep = calls(T)
+    want = [f() for f in fs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [[f(stream=st) for f in fs] for st in streams]
+        torch.cuda.synchronize()
+        for outs in got:
+            for i, (a, b) in enumerate(zip(outs, want)):
+                assert torch.equal(a, b), (T, i)
+
+
+def test_views_and_given_buffers():
+    say("mx views")
+    g = gen(5)
+    O, K = 96, 256
+    q, s = ref.rand_mx(g, (O,), K)
+    W = qm.MxMat(q.to(DEV), s.to(DEV), K)
+    wide = torch.randn(40, K + 24, generator=g).to(DEV)
+    for t in (torch.float32, torch.bfloat16):
+        x = wide.to(t)[:, 8:8 + K]
+        want = qm.qmoe_mx_matmul(W, x.contiguous())
+        out = torch.zeros(40, O + 8, dtype=t, device=DEV)
+        if t == torch.float32:                  # 8 elements in: 32 bytes, aligned
+            got = qm.qmoe_mx_matmul(W, x, out=out[:, :O])
+            assert torch.equal(got, want) and (out[:, O:] == 0).all()
+        one = qm.qmoe_mx_matmul(W, x[3])        # a single row
+        assert torch.equal(one, qm.qmoe_mx_matmul(W, x[3:4].contiguous()))
+    with pytest.raises(qm.QmoeError):
+        qm.qmoe_mx_matmul(W, wide[:, 1:1 + K])                       # misaligned rows
+    with pytest.raises(ValueError):
+        qm.qmoe_mx_matmul(W, wide.t()[:K].t()[:, ::2])
+    with pytest.raises(ValueError):
+        qm.qmoe_mx_matmul(W, wide[:, :K], out=torch.empty(40, O + 1, device=DEV))
+    with pytest.raises(ValueError):
+        qm.qmoe_mx_layer(qm.MxLayer(*[qm.MxMat(W.q[None], W.s[None], K)] * 2,
+                                    qm.MxMat(*[torch.zeros(1, K, n, dtype=torch.uint8, device=DEV) for n in (48, 3)], O)),
+                         wide[:, :K].contiguous(), torch.zeros(40, 2, dtype=torch.int32, device=DEV),
+                         torch.zeros(40, 1, device=DEV))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+def test_stack_past_four_gigabytes(kind):
+    """Expert offsets beyond 32 bits: the last experts of a strided stack of 5 GB."""
+    say(f"mx large stack {kind}")
+    g = gen(6)
+    E, O, K = 160, 64, 256
+    stride = 5 * (1 << 30) // E // 16 * 16
+    q, s = ref.rand_mx(g, (E, O), K)
+    buf = torch.empty(E * stride, dtype=torch.uint8, device=DEV)
+    big = buf.as_strided((E, O, K // 2), (stride, K // 2, 1))
+    big.copy_(q.to(DEV))
+    W = qm.MxMat.__new__(qm.MxMat)
+    small = qm.MxMat(q.to(DEV), s.to(DEV), K)
+    W.__dict__.update(small.__dict__)
+    W.keep = buf
+    W.desc = qm.qmoe_mxmat.from_buffer_copy(small.desc)
+    W.desc.q, W.desc.q_expert_stride = big.data_ptr(), stride
+    W.ref = __import__("ctypes").byref(W.desc)
+    for per in (1, 40):
+        n = E * per
+        x, x_s, _ = rows_of(kind, g, n, K)
+        offsets = torch.arange(0, n + 1, per, dtype=torch.int32, device=DEV)
+        assert torch.equal(qm.qmoe_mx_grouped(W, x, offsets, x_s=x_s), qm.qmoe_mx_grouped(small, x, offsets, x_s=x_s))
+
+
+@pytest.mark.parametrize("E,T,k", [(1024, 5, 64), (1024, 70, 16), (300, 40, 1), (1, 9, 1), (65, 3, 5)])
+def test_layer_many_experts_and_choices(E, T, k):
+    say(f"mx layer E={E} T={T} k={k}")
+    g = gen(E + T)
+    H, F = 64, 40
+    dev, (gate, up, down) = make_layer(g, E, H, F)
+    for kind in ("f32", "bf16"):
+        x = torch.randn(T, H, generator=g).to(TYPES[kind])
+        ids, w = routing(g, T, E, min(k, E))
+        want, bound = ref.layer(gate, up, down, np64(x), ids.numpy(), np64(w), parts(kind), kind == "bf16")
+        check_layer(qm.qmoe_mx_layer(dev, x.to(DEV), ids.to(DEV), w.to(DEV)), want, bound, kind, "layer")
