@@ -282,6 +282,23 @@ inline int64_t mx_max_tiles(const MxGroups &g, int bm) {
     return g.offsets ? t + (g.n < g.experts ? g.n : g.experts) : t;
 }
 
+// Rows whose parts share the 16 columns of an MFMA in mx_stream.hip.
+constexpr int MXS_PACK = 5;
+constexpr int mxs_rows(int parts) { return parts == 3 ? MXS_PACK : 16; }
+
+// Passes of two column tiles read and decode the weights half as often, but
+// make half as many blocks, of fewer waves.  They pay from 2048 inputs on, if
+// their blocks still are one per compute unit: 4096 x 4096, one and two tiles
+// (us), f32 64 rows 38 and 32, 256 rows 114 and 103; bf16 64 rows 12 and 17, 128
+// rows 20 and 17, 256 rows 35 and 28; MXFP4 256 rows 26 and 18; of 1024 inputs
+// bf16 256 rows 12 and 12.5.  Layers, whose groups often hold fewer rows than one
+// tile, lose (64 f32 tokens 374 and 391).
+inline bool mx_stream_wide(const MxGroups &g, int parts, int rows, int nb) {
+    const int64_t groups = g.offsets ? (g.n < g.experts ? g.n : g.experts) : 1;
+    const int64_t passes = groups * (g.n / groups / (2 * mxs_rows(parts)));
+    return nb >= 64 && passes * (rows / 64) >= 256;
+}
+
 // ---- launchers (host side; shapes are validated by the C ABI layer) -------
 
 hipError_t launch_mx_quantize(const void *x, bool f32, int64_t rows, int cols, int64_t ld,

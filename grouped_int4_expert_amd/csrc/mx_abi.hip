@@ -98,9 +98,9 @@ hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, i
 // have to read the weights, which the stream does faster.  Measured: one matrix
 // of 4096 x 4096, 16 to 1024 rows, each kernel alone (us):
 //   rows          16    64   128   256   512  1024
-//   f32  stream   17    38    67   114   219   419     tiles  60  84  189  192  193  198
-//   bf16 stream   8.6   12    20    35    67   130     tiles  31  36   51   51   55   56
-//   MXFP4 stream  6.2   9.1   15    26    47    91     tiles  22  24   28   28   29   31
+//   f32  stream   17    32    55   103   188   419     tiles  60  84  181  183  185  198
+//   bf16 stream   8.6   12    17    28    53   130     tiles  31  36   51   52   55   56
+//   MXFP4 stream  6.2   9.1   12    18    34    91     tiles  22  24   28   28   29   31
 // The times over 512 to 8192 inputs of calls whose blocks fit at once give each
 // block's start and its time per input, below.  8 MXFP4 groups of 96 and 200 rows,
 // 2048 x 2048: stream 21 and 42 us, tiles 19 and 26; 1024 inputs: 12 and 24, 14 and
@@ -110,12 +110,13 @@ struct TileCost {
     int slots;          // blocks the GPU holds at once
     double start, ns;   // of one block: ns at its start and end, and per input
 };
-bool takes_tiles(const MxGroups &g, int parts, int64_t rows, int64_t col_blocks, int64_t cols) {
-    static const double stream[3] = {5.3e-6, 7.5e-6, 24.4e-6};   // ns per row, weight row and input
+bool takes_tiles(const MxGroups &g, int parts, bool pair, int64_t rows, int64_t col_blocks,
+                 int64_t cols) {
+    // ns per row, weight row and input: passes of one column tile, of two
+    static const double stream[2][3] = {{5.3e-6, 7.5e-6, 24.4e-6}, {3.4e-6, 5.5e-6, 21.5e-6}};
     static const double bytes_per_ns[3] = {3000, 3600, 3100};    // weights through the tiles; streamed:
     const double streamed_per_ns = 4600, stream_start = 4000;
-    static const int pass[3] = {16, 16, 5};
-    static const TileCost cost[3][3] = {        // tiles of 32, 64, 128 rows; MXFP4: 64, 64, 128 (256 in groups)
+    static const TileCost cost[3][3] = {  // 32, 64, 128 rows; MXFP4: 64, 64, 128 (256 in groups)
         {{512, 6300, 4.2}, {512, 6300, 4.2}, {256, 9400, 4.9}},
         {{1024, 4200, 6.5}, {512, 5400, 7.4}, {512, 7700, 11.0}},
         {{768, 4800, 12.7}, {512, 5500, 19.2}, {512, 7800, 41.1}}};
@@ -129,8 +130,11 @@ bool takes_tiles(const MxGroups &g, int parts, int64_t rows, int64_t col_blocks,
     const double bytes = (double)groups * rows * cols * 17 / 32;
     const double tiles_ns = std::max((double)((blocks + c.slots - 1) / c.slots) * (c.start + c.ns * cols),
                                      bytes / bytes_per_ns[type]);
-    const double stream_ns = stream_start + std::max(stream[type] * (g.n + groups * pass[type] / 2) * rows * cols,
-                                                       bytes / streamed_per_ns);
+    const bool wide = !pair && mx_stream_wide(g, parts, (int)rows, (int)(cols / MX_BLOCK));
+    const int64_t half_pass = mxs_rows(parts) * (wide ? 2 : 1) / 2;
+    const double stream_ns =
+        stream_start + std::max(stream[wide][type] * (double)(g.n + groups * half_pass) * rows * cols,
+                                bytes / streamed_per_ns);
     return stream_ns > tiles_ns;
 }
 
@@ -139,7 +143,7 @@ hipError_t product(const MxMat &w, const MxMat &up, const MxX &x, int dtype, con
     const int parts = dtype == QMOE_MXFP4 ? 0 : parts_of(dtype);
     const int64_t rows = up.q ? 2 * (int64_t)w.rows : w.rows;
     const int64_t col_blocks = (rows + 255) / 256;
-    if (!takes_tiles(g, parts, rows, col_blocks, (int64_t)w.nb * MX_BLOCK))
+    if (!takes_tiles(g, parts, up.q != nullptr, rows, col_blocks, (int64_t)w.nb * MX_BLOCK))
         return launch_mx_stream(w, up, x, parts, g, o, st);
     if (parts == 0) return launch_mx_tile_fp4(w, x, g, o, st);
     return launch_mx_tile(w, up, x, parts, g, o, st);

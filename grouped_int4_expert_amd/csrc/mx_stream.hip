@@ -1,5 +1,6 @@
 // MXFP4 products for few rows per matrix: the weights are streamed once per
-// pass of at most 16 rows (5 f32 rows).
+// pass of at most 16 rows (5 f32 rows), or twice as many (two column tiles,
+// mx_stream_wide).
 //
 // A block takes RT row tiles of 16 weight rows and one pass; its waves split
 // the inputs into chunks of 512 (wave w takes chunks w, w + WV, ...) and meet
@@ -24,8 +25,6 @@
 
 namespace qmoe {
 
-constexpr int MXS_PACK = 5;         // f32 rows whose parts share the 16 columns
-constexpr int mxs_rows(int parts) { return parts == 3 ? MXS_PACK : 16; }   // rows per pass
 constexpr int MXS_WIDE_ROWS = 32;   // up to here blocks take two tiles, above four
 
 // The weights of a block: bases of the matrix (or the pair) and the lane's row
@@ -36,16 +35,17 @@ struct MxsWeights {
     uint32_t qo[RT], so[RT];
 };
 
-// acc[i] += tile i of the weights times x over the wave's chunks (MX: x is
-// MXFP4).
-template <bool MX, int RT, int RTM, int WV>
-__device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> &W,
-                                         const uint8_t *xv, const uint8_t *xs, int nb, int w) {
+// acc[k][i] += tile i of the weights times column tile k < USED of x over the
+// wave's chunks (MX: x is MXFP4).
+template <bool MX, int RT, int RTM, int WV, int USED, int CT>
+__device__ __forceinline__ void mxs_body(f32x4 (&acc)[CT][RT], const MxsWeights<RT> &W,
+                                         const uint8_t *const (&xv)[CT],
+                                         const uint8_t *const (&xs)[CT], int nb, int w) {
     const int quarter = lane_id() >> 4;
     const int chunks = (nb + 15) / 16;
     for (int c = w; c < chunks; c += WV) {
         u32x4 cq[4][RT];
-        uint32_t cs[RT], xc = 0;
+        uint32_t cs[RT], xc[USED] = {};
 #pragma unroll
         for (int i = 0; i < RT; i++) {
             const u32x4 v = mx_scales16(W.s[i / RTM] + W.so[i], 16 * c, nb);
@@ -57,40 +57,51 @@ __device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> 
             }
             cs[i] = mx_pick(v, quarter);
         }
-        if constexpr (MX) xc = mx_pick(mx_scales16(xs, 16 * c, nb), quarter);
+        if constexpr (MX)
+#pragma unroll
+            for (int k = 0; k < USED; k++) xc[k] = mx_pick(mx_scales16(xs[k], 16 * c, nb), quarter);
 #pragma unroll
         for (int s = 0; s < 4; s++) {
             const int b = 16 * c + 4 * s + quarter;
             if constexpr (MX) {
-                u32x4 xq = *reinterpret_cast<const u32x4 *>(xv + (int64_t)min(b, nb - 1) * 16);
-                if (b >= nb) xq = u32x4{0, 0, 0, 0};
-                const i32x8 xb = {(int)xq[0], (int)xq[1], (int)xq[2], (int)xq[3], 0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < RT; i++) {
-                    const u32x4 e = cq[s][i];
-                    const i32x8 wb = {(int)e[0], (int)e[1], (int)e[2], (int)e[3], 0, 0, 0, 0};
+                for (int k = 0; k < USED; k++) {
+                    u32x4 xq = *reinterpret_cast<const u32x4 *>(xv[k] + (int64_t)min(b, nb - 1) * 16);
+                    if (b >= nb) xq = u32x4{0, 0, 0, 0};
+                    const i32x8 xb = {(int)xq[0], (int)xq[1], (int)xq[2], (int)xq[3], 0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < RT; i++) {
+                        const u32x4 e = cq[s][i];
+                        const i32x8 wb = {(int)e[0], (int)e[1], (int)e[2], (int)e[3], 0, 0, 0, 0};
 #define MXS_STEP(n)                                                                               \
     if (s == n)                                                                                   \
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, xb, acc[i], 4, 4, n,        \
-                                                                  (int)cs[i], n, (int)xc);
-                    MXS_STEP(0) MXS_STEP(1) MXS_STEP(2) MXS_STEP(3)
+        acc[k][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, xb, acc[k][i], 4, 4, n,  \
+                                                                     (int)cs[i], n, (int)xc[k]);
+                        MXS_STEP(0) MXS_STEP(1) MXS_STEP(2) MXS_STEP(3)
 #undef MXS_STEP
+                    }
                 }
             } else {
                 // x rows hold zeros up to a whole step past their end; the steps
                 // after that are not computed
                 if (16 * c + 4 * s >= nb) break;
-                bf16x8 xf[4];
+                bf16x8 xf[USED][4];
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    xf[j] = *reinterpret_cast<const bf16x8 *>(xv + (int64_t)b * 64 + j * 16);
+                for (int k = 0; k < USED; k++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        xf[k][j] =
+                            *reinterpret_cast<const bf16x8 *>(xv[k] + (int64_t)b * 64 + j * 16);
 #pragma unroll
                 for (int i = 0; i < RT; i++) {
                     const float sc = mx_scale((cs[i] >> (8 * s)) & 255u);
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         const bf16x8 wf = __builtin_bit_cast(bf16x8, mx_decode8(cq[s][i][j], sc));
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[j], acc[i], 0, 0, 0);
+#pragma unroll
+                        for (int k = 0; k < USED; k++)
+                            acc[k][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[k][j],
+                                                                                acc[k][i], 0, 0, 0);
                     }
                 }
             }
@@ -100,24 +111,29 @@ __device__ __forceinline__ void mxs_body(f32x4 (&acc)[RT], const MxsWeights<RT> 
 
 // parts: 0, 1, 3; PAIR: tiles RT/2.. are of the second matrix (up) and the
 // block writes h = silu(g) * u.
-template <int PARTS, int RT, int WV, bool PAIR>
+template <int PARTS, int RT, int CT, int WV, bool PAIR>
 __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, MxX x, MxGroups g,
                                                             MxOut o) {
     constexpr int RTM = PAIR ? RT / 2 : RT;      // tiles of one matrix
-    __shared__ __attribute__((aligned(16))) float red[WV][RT][64][4];
+    constexpr int ROWS = mxs_rows(PARTS);        // of a column tile
+    __shared__ __attribute__((aligned(16))) float red[WV][CT][RT][64][4];
     const int ncb = ((PAIR ? o.width : W.rows) + 16 * RTM - 1) / (16 * RTM);
     MxTile t;
-    if (!mx_find(g, mxs_rows(PARTS), ncb, t)) return;
+    if (!mx_find(g, CT * ROWS, ncb, t)) return;
     const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
     const int r16 = lane & 15;
     const int o0 = t.cb * 16 * RTM;
 
-    // this lane's x row, and of f32 rows its part
+    // this lane's x row of each column tile, and of f32 rows its part
     const int part = PARTS == 3 ? min(r16 / MXS_PACK, 2) : 0;
-    const int col = min(PARTS == 3 ? r16 % MXS_PACK : r16, t.rows - 1);
-    const int64_t src = max(mx_source(g, x, t.pos0 + col), (int64_t)0);
-    const uint8_t *xv = x.v + src * x.ld + (int64_t)part * x.width * 2;
-    const uint8_t *xs = PARTS == 0 ? x.s + src * W.nb : nullptr;
+    const uint8_t *xv[CT], *xs[CT];
+#pragma unroll
+    for (int k = 0; k < CT; k++) {
+        const int col = min(k * ROWS + (PARTS == 3 ? r16 % MXS_PACK : r16), t.rows - 1);
+        const int64_t src = max(mx_source(g, x, t.pos0 + col), (int64_t)0);
+        xv[k] = x.v + src * x.ld + (int64_t)part * x.width * 2;
+        xs[k] = PARTS == 0 ? x.s + src * W.nb : nullptr;
+    }
 
     MxsWeights<RT> wt;
     wt.q[0] = W.q + (int64_t)t.e * W.q_stride;
@@ -131,27 +147,35 @@ __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, Mx
         wt.so[i] = row * (uint32_t)W.nb;
     }
 
-    f32x4 acc[RT];
+    f32x4 acc[CT][RT];
 #pragma unroll
-    for (int i = 0; i < RT; i++) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    mxs_body<PARTS == 0, RT, RTM, WV>(acc, wt, xv, xs, W.nb, w);
+    for (int k = 0; k < CT; k++)
+#pragma unroll
+        for (int i = 0; i < RT; i++) acc[k][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (CT == 1 || t.rows > ROWS)
+        mxs_body<PARTS == 0, RT, RTM, WV, CT>(acc, wt, xv, xs, W.nb, w);
+    else
+        mxs_body<PARTS == 0, RT, RTM, WV, 1>(acc, wt, xv, xs, W.nb, w);
 
 #pragma unroll
-    for (int i = 0; i < RT; i++) *reinterpret_cast<f32x4 *>(red[w][i][lane]) = acc[i];
+    for (int k = 0; k < CT; k++)
+#pragma unroll
+        for (int i = 0; i < RT; i++) *reinterpret_cast<f32x4 *>(red[w][k][i][lane]) = acc[k][i];
     __syncthreads();
     // output (row c of the pass, weight row o0 + r): accumulator r % 4 of lane
     // (r % 16 / 4) * 16 + c of tile r / 16
-    for (int idx = threadIdx.x; idx < 16 * RTM * 16; idx += WV * 64) {
+    for (int idx = threadIdx.x; idx < 16 * RTM * CT * ROWS; idx += WV * 64) {
         const int r = idx % (16 * RTM), c = idx / (16 * RTM);
         if (c >= t.rows) break;
-        const int ln = ((r & 15) >> 2) * 16 + c, v = r & 3, n = o0 + r;
+        const int ct = CT == 1 ? 0 : c / ROWS;
+        const int ln = ((r & 15) >> 2) * 16 + (c - ct * ROWS), v = r & 3, n = o0 + r;
         float a = 0.f, u = 0.f;
 #pragma unroll
         for (int p = 0; p < (PARTS == 3 ? 3 : 1); p++)
 #pragma unroll
             for (int k = 0; k < WV; k++) {
-                a += red[k][r >> 4][ln + p * MXS_PACK][v];
-                if (PAIR) u += red[k][RTM + (r >> 4)][ln + p * MXS_PACK][v];
+                a += red[k][ct][r >> 4][ln + p * MXS_PACK][v];
+                if (PAIR) u += red[k][ct][RTM + (r >> 4)][ln + p * MXS_PACK][v];
             }
         const int pos = t.pos0 + c;
         if constexpr (PAIR) {
@@ -176,13 +200,13 @@ __global__ void __launch_bounds__(WV * 64) mx_stream_kernel(MxMat W, MxMat U, Mx
     }
 }
 
-template <int PARTS, int RT, int WV, bool PAIR>
+template <int PARTS, int RT, int CT, int WV, bool PAIR>
 static hipError_t go(const MxMat &w, const MxMat &up, const MxX &x, const MxGroups &g,
                      const MxOut &out, hipStream_t st) {
     constexpr int RTM = PAIR ? RT / 2 : RT;
     const int64_t ncb = ((PAIR ? out.width : w.rows) + 16 * RTM - 1) / (16 * RTM);
-    const dim3 grid(mx_grid(mx_max_tiles(g, mxs_rows(PARTS)) * ncb));
-    hipLaunchKernelGGL((mx_stream_kernel<PARTS, RT, WV, PAIR>), grid, dim3(WV * 64), 0, st, w, up, x,
+    const dim3 grid(mx_grid(mx_max_tiles(g, CT * mxs_rows(PARTS)) * ncb));
+    hipLaunchKernelGGL((mx_stream_kernel<PARTS, RT, CT, WV, PAIR>), grid, dim3(WV * 64), 0, st, w, up, x,
                        g, out);
     return hipGetLastError();
 }
@@ -193,27 +217,31 @@ static hipError_t go(const MxMat &w, const MxMat &up, const MxX &x, const MxGrou
 // 128-expert projection: 8 waves 107 us, 4 waves 89, 2 waves 93, 1 wave 93), two
 // for f32 rows, whose passes hold fewer rows (64-token layer: gate+up 4 waves
 // 243 us, 2 waves 241; down 3 waves 134, 1 wave 118).
-template <int PARTS, int RT, bool PAIR>
+template <int PARTS, int RT, int CT, bool PAIR>
 static hipError_t by_width(const MxMat &w, const MxMat &up, const MxX &x, const MxGroups &g,
                            const MxOut &out, hipStream_t st) {
     const int chunks = (w.nb + 15) / 16;
     if constexpr (RT == 4 && PARTS == 3) {
-        if (chunks <= 3) return go<PARTS, RT, 1, PAIR>(w, up, x, g, out, st);
-        return go<PARTS, RT, 2, PAIR>(w, up, x, g, out, st);
+        if (chunks <= 3) return go<PARTS, RT, CT, 1, PAIR>(w, up, x, g, out, st);
+        return go<PARTS, RT, CT, 2, PAIR>(w, up, x, g, out, st);
     } else {
-        if (chunks == 1) return go<PARTS, RT, 1, PAIR>(w, up, x, g, out, st);
-        if (chunks == 2) return go<PARTS, RT, 2, PAIR>(w, up, x, g, out, st);
-        if (chunks == 3) return go<PARTS, RT, 3, PAIR>(w, up, x, g, out, st);
-        if (RT == 4 || chunks == 4) return go<PARTS, RT, 4, PAIR>(w, up, x, g, out, st);
-        return go<PARTS, RT, 8, PAIR>(w, up, x, g, out, st);
+        if (chunks == 1) return go<PARTS, RT, CT, 1, PAIR>(w, up, x, g, out, st);
+        if (chunks == 2) return go<PARTS, RT, CT, 2, PAIR>(w, up, x, g, out, st);
+        if (chunks == 3) return go<PARTS, RT, CT, 3, PAIR>(w, up, x, g, out, st);
+        if constexpr (RT == 2)
+            if (chunks > 4) return go<PARTS, RT, CT, 8, PAIR>(w, up, x, g, out, st);
+        return go<PARTS, RT, CT, 4, PAIR>(w, up, x, g, out, st);
     }
 }
 
 template <int PARTS, bool PAIR>
 static hipError_t by_rows(const MxMat &w, const MxMat &up, const MxX &x, const MxGroups &g,
                           const MxOut &out, hipStream_t st) {
-    if (g.n <= MXS_WIDE_ROWS) return by_width<PARTS, 2, PAIR>(w, up, x, g, out, st);
-    return by_width<PARTS, 4, PAIR>(w, up, x, g, out, st);
+    if (g.n <= MXS_WIDE_ROWS) return by_width<PARTS, 2, 1, PAIR>(w, up, x, g, out, st);
+    if constexpr (!PAIR)
+        if (mx_stream_wide(g, PARTS, w.rows, w.nb))
+            return by_width<PARTS, 4, 2, false>(w, up, x, g, out, st);
+    return by_width<PARTS, 4, 1, PAIR>(w, up, x, g, out, st);
 }
 
 hipError_t launch_mx_stream(const MxMat &w, const MxMat &up, const MxX &x, int parts,

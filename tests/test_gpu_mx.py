@@ -1,6 +1,8 @@
 """The MXFP4 entry points on the GPU against 64-bit references: rounding to
 the format and back bit for bit, the products and the routed layer within
 bounds that follow each rounded quantity (mx_ref)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -415,6 +417,31 @@ def test_quantize_route_group_and_layer_together(T):
     assert float((a4 - av).norm() / av.norm()) <= 2.0 ** -20
 
 
+# Passes of two column tiles (2048 inputs and more, a block per compute unit): full passes, a last one of
+# one tile, groups of uneven sizes with empty and single-row ones among them.
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("batch,rows,cols", [(130, 4100, 2049), (257, 4100, 2080), (300, 4100, 2177)])
+def test_matmul_wide_passes(kind, batch, rows, cols):
+    test_matmul(kind, "f32", batch, rows, cols)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+def test_grouped_wide_passes(kind):
+    say(f"mx grouped wide passes {kind}")
+    g = gen(8)
+    E, O, K = 9, 2060, 2048
+    off = torch.tensor([0, 0, 1, 150, 37, 17, 16, 130, 0, 90]).cumsum(0).to(torch.int32)
+    n = int(off[-1])
+    q, s = ref.rand_mx(g, (E, O), K)
+    x, x_s, xv = rows_of(kind, g, n, K)
+    y = qm.qmoe_mx_grouped(qm.MxMat(q.to(DEV), s.to(DEV), K), x, off.to(DEV), x_s=x_s)
+    want, m = np.zeros((n, O)), np.zeros((n, O))
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        want[a:b], m[a:b] = ref.product(ref.decode(q[e], s[e], K), xv[a:b])
+    check(y, want, ref.sum_bound(K, parts(kind)) * m, y.dtype, "grouped wide passes")     # bf16 of bf16 rows
+
+
 # ------------------------------------------------- streams, graphs, large stacks
 
 def calls(T, seed=77, E=12, H=384, F=224, k=3):
@@ -427,7 +454,6 @@ def calls(T, seed=77, E=12, H=384, F=224, k=3):
     wl = qm.qmoe_worklist(ids, E)
     q, s = qm.qmoe_mx_quantize(xd)
     one = qm.MxMat(layer.gate.q[1], layer.gate.s[1], H)
-    st = {}
     return [lambda **kw: qm.qmoe_mx_quantize(xb, **kw)[0],
             lambda **kw: qm.qmoe_mx_dequantize(q, s, H, **kw),
             lambda **kw: qm.qmoe_mx_matmul(one, xd, **kw),
@@ -436,7 +462,7 @@ def calls(T, seed=77, E=12, H=384, F=224, k=3):
             lambda **kw: qm.qmoe_mx_grouped(layer.up, xb, wl["offsets"], pairs=wl["pairs"], k=k, **kw),
             lambda **kw: qm.qmoe_mx_grouped(layer.up, q, wl["offsets"], pairs=wl["pairs"], k=k, x_s=s, **kw),
             lambda **kw: qm.qmoe_mx_layer(layer, xd, ids, w, **kw),
-            lambda **kw: qm.qmoe_mx_layer(layer, xb, ids, w, **kw)], (xd, xb, st)
+            lambda **kw: qm.qmoe_mx_layer(layer, xb, ids, w, **kw)], (xd, xb)
 
 
 @pytest.mark.parametrize("T", [1, 7, 60, 3000])
@@ -444,7 +470,7 @@ def test_replayed_graphs(T):
     """Two captured graphs of the same calls (each with workspaces of its own), replayed in turn with eager
     work between: every replay gives the eager results of the inputs as they are then."""
     say(f"mx graphs T={T}")
-    fs, (xd, xb, _) = calls(T)
+    fs, (xd, xb) = calls(T)
     for f in fs:
         f()
     torch.cuda.synchronize()
@@ -529,7 +555,7 @@ def test_stack_past_four_gigabytes(kind):
     W.keep = buf
     W.desc = qm.qmoe_mxmat.from_buffer_copy(small.desc)
     W.desc.q, W.desc.q_expert_stride = big.data_ptr(), stride
-    W.ref = __import__("ctypes").byref(W.desc)
+    W.ref = ctypes.byref(W.desc)
     for per in (1, 40):
         n = E * per
         x, x_s, _ = rows_of(kind, g, n, K)
