@@ -324,10 +324,12 @@ hipError_t launch_mx_few(const MxMat &w, const MxMat &up, int parts, const MxFew
 hipError_t launch_mx_few_down(const MxMat &d, int parts, const MxFew &f, const uint8_t *h,
                               int64_t h_ld, int width, const float *topk_w, int tokens, void *out,
                               hipStream_t st);
-hipError_t launch_mx_tile(const MxMat &w, const MxMat &up, const MxX &x, int parts,
+// size: 0 .. 2, tiles of 32, 64, 128 rows (128 not of three parts).
+hipError_t launch_mx_tile(const MxMat &w, const MxMat &up, const MxX &x, int parts, int size,
                           const MxGroups &g, const MxOut &out, hipStream_t st);
-hipError_t launch_mx_tile_fp4(const MxMat &w, const MxX &x, const MxGroups &g, const MxOut &out,
-                              hipStream_t st);
+// size: 0 .. 2, tiles of 64, 128, 256 rows.
+hipError_t launch_mx_tile_fp4(const MxMat &w, const MxX &x, int size, const MxGroups &g,
+                              const MxOut &out, hipStream_t st);
 // out[t] = sum_j y[inv[t * k + j]] in pick order (f32 sums), as f32 or bf16.
 hipError_t launch_mx_combine(const float *y, const int32_t *inv, int tokens, int k, int cols,
                              void *out, bool f32, hipStream_t st);

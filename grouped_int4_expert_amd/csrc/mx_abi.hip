@@ -91,62 +91,84 @@ hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, i
                            st);
 }
 
-// Which kernel a product takes: passes that stream the weights (mx_stream.hip),
-// or tiles (mx_tile.hip, mx_tile_fp4.hip).  The stream's time grows with rows x
-// weights (every group's last pass half empty); a tile's with the inputs alone,
-// as long as the tiles of a call fit the GPU at once, and is then repeated; both
-// have to read the weights, which the stream does faster.  Measured: one matrix
-// of 4096 x 4096, 16 to 1024 rows, each kernel alone (us):
-//   rows          16    64   128   256   512  1024
-//   f32  stream   17    32    55   103   188   419     tiles  60  84  181  183  185  198
-//   bf16 stream   8.6   12    17    28    53   130     tiles  31  36   51   52   55   56
-//   MXFP4 stream  6.2   9.1   12    18    34    91     tiles  22  24   28   28   29   31
-// The times over 512 to 8192 inputs of calls whose blocks fit at once give each
-// block's start and its time per input, below.  8 MXFP4 groups of 96 and 200 rows,
-// 2048 x 2048: stream 21 and 42 us, tiles 19 and 26; 1024 inputs: 12 and 24, 14 and
-// 20.  A layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 405 at
-// 64 tokens, 480 and 451 at 96; bf16 310 and 338 at 96, 412 and 380 at 200.
+// Which kernel a product takes: passes that stream the weights (mx_stream.hip;
+// -1), or tiles (mx_tile.hip, mx_tile_fp4.hip) of size 0, 1 or 2.  The stream's
+// time grows with rows x weights (every group's last pass half empty).  A tile's
+// grows with the inputs alone while every compute unit has one; each further
+// tile of a unit adds about as much again, less for small tiles, which hide one
+// another's waits.  Both have to read the weights, which the stream does faster.
+// Measured: one matrix of 4096 x 4096 (us; tiles by the rows of one):
+//   rows            64   128   256   512  1024  2048  4096
+//   f32  stream     32    55   102   188   419
+//        tiles 32   63    63    66    68   104   204   379
+//              64   84    87    90    91   100   184   354
+//             128        181   182   184   188   228   401      (spills; not built)
+//   bf16 stream     12    17    28    53   130
+//        tiles 32   31    31    32    36    51    97   189
+//              64   36    36    36    40    43    72   143
+//             128         50    51    54    56    63   125
+//   MXFP4 stream   9.1    12    18    34    91
+//        tiles 64   25    24    25    26    27    49    93
+//             128         27    28    29    31    35    65
+//             256               36    37    40    43    57
+// the same at 1024 inputs: f32 512 rows 25, 31, 55, bf16 12, 14, 20.  Groups,
+// bf16: 8 of 128 rows, 2048 x 4096, tiles 37, 41, 55; 128 of 64, 1536 x 4096, 184,
+// 145, 181; 128 of 128, 1536 x 1024, 83, 67, 59.  Ragged MXFP4 groups of more than
+// 64 rows take 256-row tiles, which compute 64, 128 or 192 rows where no more are
+// left.  A layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 405 at
+// 64 tokens, 480 and 451 at 96; bf16 310 and 338 at 96, 412 and 380 at 200; tiles of
+// 32, 64, 128 rows: 1024 tokens f32 1048, 1105, 1752, bf16 647, 561, 614; 2048
+// tokens f32 1871, 1837, 2437, bf16 1098, 901, 848.
 struct TileCost {
-    int slots;          // blocks the GPU holds at once
-    double start, ns;   // of one block: ns at its start and end, and per input
+    int rows;
+    double start, first, more;   // ns; per input of a unit's first tile, of a further one
 };
-bool takes_tiles(const MxGroups &g, int parts, bool pair, int64_t rows, int64_t col_blocks,
-                 int64_t cols) {
+int tile_size(const MxGroups &g, int parts, bool pair, int64_t rows, int64_t cols) {
+    static const TileCost cost[3][3] = {
+        {{64, 6300, 4.8, 5.4}, {128, 9400, 5.8, 7.3}, {256, 11600, 7.9, 7.9}},
+        {{32, 4200, 7.5, 5.4}, {64, 5400, 8.8, 8.3}, {128, 7700, 12.3, 13.3}},
+        {{32, 4800, 14.2, 10.0}, {64, 5500, 20.6, 18.0}, {}}};
     // ns per row, weight row and input: passes of one column tile, of two
     static const double stream[2][3] = {{5.3e-6, 7.5e-6, 24.4e-6}, {3.4e-6, 5.5e-6, 21.5e-6}};
-    static const double bytes_per_ns[3] = {3000, 3600, 3100};    // weights through the tiles; streamed:
+    static const double bytes_per_ns[3] = {4100, 3600, 3100};    // weights through the tiles; streamed:
     const double streamed_per_ns = 4600, stream_start = 4000;
-    static const TileCost cost[3][3] = {  // 32, 64, 128 rows; MXFP4: 64, 64, 128 (256 in groups)
-        {{512, 6300, 4.2}, {512, 6300, 4.2}, {256, 9400, 4.9}},
-        {{1024, 4200, 6.5}, {512, 5400, 7.4}, {512, 7700, 11.0}},
-        {{768, 4800, 12.7}, {512, 5500, 19.2}, {512, 7800, 41.1}}};
     const int type = parts == 3 ? 2 : parts;
     const int64_t groups = g.offsets ? (g.n < g.experts ? g.n : g.experts) : 1;
-    const int64_t per = (g.n + groups - 1) / groups;
-    const int size = per <= 32 ? 0 : per <= 64 ? 1 : 2;
-    const int64_t tile = parts == 0 ? (size < 2 ? 64 : g.offsets ? 256 : 128) : 32 << size;
-    const int64_t blocks = groups * ((per + tile - 1) / tile) * col_blocks;
-    const TileCost c = cost[type][size];
+    int best = 0;
+    double tiles_ns = 0;
+    for (int i = 0; i < 3; i++) {
+        const TileCost &c = cost[type][i];
+        if (c.rows == 0) continue;
+        // ragged groups: half a tile of each is empty
+        const int64_t tiles = g.offsets ? std::max(groups, g.n / c.rows + groups / 2)
+                                        : (g.n + c.rows - 1) / c.rows;
+        const int64_t blocks = tiles * ((rows + 255) / 256);
+        const double turns = std::max((double)blocks / 256, 1.0);     // tiles of a unit
+        const double ns = c.start + (c.first + (turns - 1) * c.more) * cols;
+        if (type == 0 && g.offsets && (i == 1 || (i == 2 && g.n <= 64 * groups))) continue;
+        if (i == 0 || ns < tiles_ns) {
+            best = i;
+            tiles_ns = ns;
+        }
+    }
     const double bytes = (double)groups * rows * cols * 17 / 32;
-    const double tiles_ns = std::max((double)((blocks + c.slots - 1) / c.slots) * (c.start + c.ns * cols),
-                                     bytes / bytes_per_ns[type]);
+    tiles_ns = std::max(tiles_ns, bytes / bytes_per_ns[type]);
     const bool wide = !pair && mx_stream_wide(g, parts, (int)rows, (int)(cols / MX_BLOCK));
     const int64_t half_pass = mxs_rows(parts) * (wide ? 2 : 1) / 2;
     const double stream_ns =
         stream_start + std::max(stream[wide][type] * (double)(g.n + groups * half_pass) * rows * cols,
                                 bytes / streamed_per_ns);
-    return stream_ns > tiles_ns;
+    return stream_ns > tiles_ns ? best : -1;
 }
 
 hipError_t product(const MxMat &w, const MxMat &up, const MxX &x, int dtype, const MxGroups &g,
                    const MxOut &o, hipStream_t st) {
     const int parts = dtype == QMOE_MXFP4 ? 0 : parts_of(dtype);
     const int64_t rows = up.q ? 2 * (int64_t)w.rows : w.rows;
-    const int64_t col_blocks = (rows + 255) / 256;
-    if (!takes_tiles(g, parts, up.q != nullptr, rows, col_blocks, (int64_t)w.nb * MX_BLOCK))
-        return launch_mx_stream(w, up, x, parts, g, o, st);
-    if (parts == 0) return launch_mx_tile_fp4(w, x, g, o, st);
-    return launch_mx_tile(w, up, x, parts, g, o, st);
+    const int size = tile_size(g, parts, up.q != nullptr, rows, (int64_t)w.nb * MX_BLOCK);
+    if (size < 0) return launch_mx_stream(w, up, x, parts, g, o, st);
+    if (parts == 0) return launch_mx_tile_fp4(w, x, size, g, o, st);
+    return launch_mx_tile(w, up, x, parts, size, g, o, st);
 }
 
 // Grids stay below 2^31 blocks: tiles (16 rows and more) times column blocks

@@ -276,11 +276,10 @@ static hipError_t go(const MxMat &w, const MxX &x, const MxGroups &g, const MxOu
     return hipGetLastError();
 }
 
-hipError_t launch_mx_tile_fp4(const MxMat &w, const MxX &x, const MxGroups &g, const MxOut &out,
-                              hipStream_t st) {
-    const int64_t per = (g.n + g.experts - 1) / g.experts;    // rows per group on average
-    if (per <= 64) return go<2>(w, x, g, out, st);
-    if (!g.offsets) return go<4>(w, x, g, out, st);
+hipError_t launch_mx_tile_fp4(const MxMat &w, const MxX &x, int size, const MxGroups &g,
+                              const MxOut &out, hipStream_t st) {
+    if (size == 0) return go<2>(w, x, g, out, st);
+    if (size == 1) return go<4>(w, x, g, out, st);
     return go<8>(w, x, g, out, st);
 }
 
