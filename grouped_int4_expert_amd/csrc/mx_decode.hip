@@ -13,6 +13,12 @@
 //    its own, and the waves' sums are added in order (no atomics, no second
 //    launch).
 // The weights go to the matrix cores as in mx_stream.hip.
+//
+// One f32 token, 8 of 128 experts 4096 / 1536: gate and up 16 us (53 MB), down 10
+// us (27 MB); one row times 4096 x 4096 5 us (8.9 MB).  Calls this short are bound
+// by the chain launch, x to LDS, weights, sums, not by the bytes (53 MB at the
+// rate of a large copy: 10 us): the scale loads cost 3 us of the 16, the last
+// chunks' products and sums 4, and other shapes of the weight loads change nothing.
 #include <atomic>
 
 #include "mx.h"

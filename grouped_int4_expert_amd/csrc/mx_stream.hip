@@ -21,6 +21,14 @@
 // L2); RT sets how often: what bounds this kernel, beside memory, is the
 // number of load instructions.  Columns past the pass read its last row and
 // are not stored.
+//
+// 64 tokens, 128 experts, top-8, 1536 x 4096, bf16: 93 us, 4.6 TB/s of weights;
+// a 64-token f32 layer (hidden 4096, inter 1536): gate and up 250-264 us, down
+// 128-131 us (3.3 TB/s).  There gate and up take 197 us with every x load at one
+// address, 167 us with every weight load at one, and as long with the decoding
+// left out: what the f32 passes pay beside the weights is x from L2, three parts
+// of each row.  Tried and not faster: eight tiles a wave, waves of a block on
+// other rows at the same inputs, x stored in the order of its loads.
 #include "mx.h"
 
 namespace qmoe {

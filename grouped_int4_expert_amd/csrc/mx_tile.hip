@@ -9,6 +9,12 @@
 // operands of the unit's two stages; with three parts the codes stay in
 // registers for all of them.  Scale bytes come eight of a row at a time, two
 // units ahead.
+//
+// 8192 tokens, 128 experts 4096 / 1536, top-8, bf16 (128-row tiles): gate and up
+// 1.41 ms (1.17 PFLOP/s), down 0.89 ms (0.92 PFLOP/s, 0.3 ms of it the f32 rows for
+// the sum).  Gate and up without any load take 1.15 ms, their MFMAs alone would
+// take 0.69: the decoding and the LDS reads issued beside the MFMAs bound this
+// kernel, more so with smaller tiles, which decode the same codes more often.
 #include "mx_tile.h"
 
 namespace qmoe {

@@ -18,6 +18,11 @@
 // read from LDS and three later stages are in flight (two, with x operands
 // read half a stage ahead, where more than 128 rows fill the registers); the
 // scale bytes of the next quad are fetched during this one.
+//
+// 2048 rows times 4096 x 4096: 31 us, 2.2 PFLOP/s; 16384 rows in 128 ragged groups
+// times 1536 x 4096: 158 us, 1.3 PFLOP/s, 3.0 TB/s.  Bound by the address path: a
+// load instruction takes about 28 cycles of a compute unit for 16 lines and 100
+// for the 64 lines of scale bytes, whose rows lie nb bytes apart.
 #include "mx_tile.h"
 
 namespace qmoe {
