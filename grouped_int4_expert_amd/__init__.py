@@ -611,12 +611,16 @@ def _rows(t, name):
     if t.dtype not in _MX_TYPES:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     shape = t.shape
+    if not 1 <= len(shape) <= 2 or (shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be [rows, cols] with dense rows")
     if len(shape) == 1:
         return t.data_ptr(), 1, shape[0]
-    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, cols] with dense rows")
     rows, cols = shape
-    return t.data_ptr(), rows, max(t.stride(0), cols) if rows > 1 else cols
+    if rows <= 1:
+        return t.data_ptr(), rows, cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows may not overlap (an expanded tensor has to be made contiguous)")
+    return t.data_ptr(), rows, t.stride(0)
 
 
 def _same_device(device, **tensors):

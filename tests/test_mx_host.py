@@ -181,3 +181,22 @@ def test_reference_by_hand():
     out, bound = ref.layer(eye, eye, eye, np.array([[1.0, -2.0]]), np.array([[0, 7]]), np.array([[0.5, 0.5]]), 1, False)
     want = 0.5 * np.array([1 / (1 + np.exp(-1.0)), 4 / (1 + np.exp(2.0))])
     assert np.allclose(out[0], want, rtol=1e-14) and (bound > 0).all()
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on a device, for the checks before a launch."""
+    is_cuda = property(lambda self: True)
+
+
+def test_rows_of_views():
+    wide = torch.zeros(6, 40).as_subclass(OnDevice)
+    assert q._rows(wide, "x")[1:] == (6, 40)
+    assert q._rows(wide[:, 8:24], "x")[1:] == (6, 40)
+    assert q._rows(wide[::2, :8], "x")[1:] == (3, 80)
+    assert q._rows(wide[2], "x")[1:] == (1, 40)
+    assert q._rows(wide[:, 3:4], "x")[1:] == (6, 40)
+    assert q._rows(wide[:1].expand(1, 40), "x")[1:] == (1, 40)
+    for bad in (wide[:1].expand(6, 40), wide[0].expand(3, 40), wide.as_strided((5, 40), (8, 1)), wide[:, 3],
+                wide.t(), wide[:, ::2], wide.reshape(2, 3, 40), wide[0, 0]):
+        with pytest.raises(ValueError):
+            q._rows(bad, "x")
