@@ -574,3 +574,37 @@ def test_layer_many_experts_and_choices(E, T, k):
         ids, w = routing(g, T, E, min(k, E))
         want, bound = ref.layer(gate, up, down, np64(x), ids.numpy(), np64(w), parts(kind), kind == "bf16")
         check_layer(qm.qmoe_mx_layer(dev, x.to(DEV), ids.to(DEV), w.to(DEV)), want, bound, kind, "layer")
+
+
+@pytest.mark.parametrize("T,H,F", [(1, 16384, 64), (2, 20001, 70), (1, 64, 8192), (3, 100, 12000), (40, 9000, 48)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_layer_wide_sides(kind, T, H, F):
+    """Sides whose rows need more than 64 KB of LDS in the decode kernels, or do not fit at all."""
+    say(f"mx layer wide {kind} T={T} {H} / {F}")
+    g = gen(H + F)
+    dev, (gate, up, down) = make_layer(g, 3, H, F)
+    x = torch.randn(T, H, generator=g).to(TYPES[kind])
+    ids, w = routing(g, T, 3, 2)
+    want, bound = ref.layer(gate, up, down, np64(x), ids.numpy(), np64(w), parts(kind), kind == "bf16")
+    check_layer(qm.qmoe_mx_layer(dev, x.to(DEV), ids.to(DEV), w.to(DEV)), want, bound, kind, "layer")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_nonfinite_rows_in_tiles(kind):
+    """A NaN or infinity stays in its own row where a tile holds it beside others."""
+    say(f"mx non-finite rows {kind}")
+    g = gen(12)
+    E, O, K, n = 4, 700, 512, 2600
+    q, s = ref.rand_mx(g, (E, O), K)
+    off = torch.tensor([0, 900, 900, 1700, n], dtype=torch.int32, device=DEV)
+    x = torch.randn(n, K, generator=g).to(TYPES[kind])
+    bad = x.clone()
+    rows = [3, 77, 901, 1699, 2599]
+    for r, v in zip(rows, (float("nan"), float("inf"), -float("inf"), float("nan"), float("inf"))):
+        bad[r, (r * 7) % K] = v
+    W = qm.MxMat(q.to(DEV), s.to(DEV), K)
+    a, b = (qm.qmoe_mx_grouped(W, t.to(DEV), off, out_dtype=torch.float32).cpu() for t in (x, bad))
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[rows] = False
+    assert torch.equal(a[keep], b[keep])
+    assert not torch.isfinite(b[rows]).any()
