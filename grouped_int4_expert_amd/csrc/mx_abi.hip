@@ -100,7 +100,7 @@ hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, i
 // Measured: one matrix of 4096 x 4096 (us; tiles by the rows of one):
 //   rows            64   128   256   512  1024  2048  4096
 //   f32  stream     32    55   102   188   419
-//        tiles 32   63    63    66    68   104   204   379
+//        tiles 32   54    56    58    61   100   191   371
 //              64   84    87    90    91   100   184   354
 //             128        181   182   184   188   228   401      (spills; not built)
 //   bf16 stream     12    17    28    53   130
@@ -111,14 +111,14 @@ hipError_t operand(int dtype, const void *x, const uint8_t *x_s, int64_t rows, i
 //        tiles 64   25    24    25    26    27    49    93
 //             128         27    28    29    31    35    65
 //             256               36    37    40    43    57
-// the same at 1024 inputs: f32 512 rows 25, 31, 55, bf16 12, 14, 20.  Groups,
+// the same at 1024 inputs: f32 512 rows 24, 31, 55, bf16 12, 14, 20.  Groups,
 // bf16: 8 of 128 rows, 2048 x 4096, tiles 37, 41, 55; 128 of 64, 1536 x 4096, 184,
 // 145, 181; 128 of 128, 1536 x 1024, 83, 67, 59.  Ragged MXFP4 groups of more than
 // 64 rows take 256-row tiles, which compute 64, 128 or 192 rows where no more are
-// left.  A layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 405 at
-// 64 tokens, 480 and 451 at 96; bf16 310 and 338 at 96, 412 and 380 at 200; tiles of
-// 32, 64, 128 rows: 1024 tokens f32 1048, 1105, 1752, bf16 647, 561, 614; 2048
-// tokens f32 1871, 1837, 2437, bf16 1098, 901, 848.
+// left.  A layer of 128 experts 4096 / 1536, top-8: f32 stream 374 us, tiles 409 at
+// 64 tokens, 480 and 430 at 96; bf16 310 and 338 at 96, 412 and 380 at 200; tiles of
+// 32, 64, 128 rows: 1024 tokens f32 1045, 1105, 1752, bf16 647, 561, 614; 2048
+// tokens f32 1852, 1837, 2437, bf16 1098, 901, 848.
 struct TileCost {
     int rows;
     double start, first, more;   // ns; per input of a unit's first tile, of a further one
@@ -127,7 +127,7 @@ int tile_size(const MxGroups &g, int parts, bool pair, int64_t rows, int64_t col
     static const TileCost cost[3][3] = {
         {{64, 6300, 4.8, 5.4}, {128, 9400, 5.8, 7.3}, {256, 11600, 7.9, 7.9}},
         {{32, 4200, 7.5, 5.4}, {64, 5400, 8.8, 8.3}, {128, 7700, 12.3, 13.3}},
-        {{32, 4800, 14.2, 10.0}, {64, 5500, 20.6, 18.0}, {}}};
+        {{32, 4800, 12.5, 10.0}, {64, 5500, 20.6, 18.0}, {}}};
     // ns per row, weight row and input: passes of one column tile, of two
     static const double stream[2][3] = {{5.3e-6, 7.5e-6, 24.4e-6}, {3.4e-6, 5.5e-6, 21.5e-6}};
     static const double bytes_per_ns[3] = {4100, 3600, 3100};    // weights through the tiles; streamed:

@@ -39,17 +39,23 @@ __device__ __forceinline__ u32x2 mxt_scales8(const uint8_t *row, int b0, int nb,
 }
 
 template <int TF, int PARTS, bool PAIR>
-__global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat U, MxX x,
+__global__ void __launch_bounds__(MXT_THREADS, TF == 1 ? 3 : 2) mx_tile_kernel(MxMat W, MxMat U, MxX x,
                                                                 MxGroups g, MxOut o) {
     constexpr int WF = MXT_WF;
     constexpr int WROWS = PAIR ? 128 : 256;      // weight rows of one matrix per block
     constexpr int SPU = 2 * PARTS;               // stages per unit
+    // Stages in the ring: four; a 32-row tile of three parts, whose stages are the
+    // shortest, needs eight to cover the way to memory (512 rows, 4096 x 4096, 69 ->
+    // 61 us; with registers for three blocks of a unit a 1024-token layer 1065 -> 1029).
+    constexpr int DEPTH = TF == 1 && PARTS == 3 ? 8 : 4;
     // loads a wave surely issued after those of a stage and before it waits for it
-    constexpr int NEWER = 2 * TF + (PARTS == 1 ? 2 * WF : 0);
+    constexpr int NEWER = (DEPTH - 2) * TF + (PARTS == 1 ? 2 * WF : 0);
     constexpr int VALU = (16 + TF * WF - 1) / (TF * WF);   // vector instructions after each MFMA
     // one array per stage: reads of a stage then do not wait for loads into another
     __shared__ __attribute__((aligned(1024))) uint8_t s0[TF * 4096], s1[TF * 4096], s2[TF * 4096],
         s3[TF * 4096];
+    constexpr int MORE = DEPTH == 8 ? TF * 4096 : 16;
+    __shared__ __attribute__((aligned(1024))) uint8_t s4[MORE], s5[MORE], s6[MORE], s7[MORE];
     const int ncb = ((PAIR ? o.width : W.rows) + WROWS - 1) / WROWS;
     MxTile t;
     if (!mx_find(g, 32 * TF, ncb, t)) return;
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
     // their MFMAs run; before step 3 the next stage is synchronised (this wave's
     // LDS reads are done; its own loads of the next stage have landed when only
     // those issued after them are outstanding; barrier), the loads of stage
-    // s + 4 go into the stage just read, and step 3 reads the next stage's
+    // s + DEPTH go into the stage just read, and step 3 reads the next stage's
     // first operands.  A unit's last stage frees its codes' registers for the
     // unit after the next.
     auto stage = [&](int u0, int s, uint8_t *cur, uint8_t *next) {
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
         MXT_WAIT_LDS();
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(NEWER));
         __builtin_amdgcn_s_barrier();
-        issue_x(u0, s + 4, cur);
+        issue_x(u0, s + DEPTH, cur);
         if (s % SPU == SPU - 1) issue_w(u0 + s / SPU + 2, s / SPU);
         if (s == 2 * SPU - 1) {
 #pragma unroll
@@ -185,9 +191,9 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
         mfmas(1);
         mxt_interleave<TF * WF, TF, VALU>();
     };
-    uint8_t *const ring[4] = {s0, s1, s2, s3};
+    uint8_t *const ring[8] = {s0, s1, s2, s3, s4, s5, s6, s7};
 #pragma unroll
-    for (int s = 0; s < 4; s++) issue_x(0, s, ring[s]);
+    for (int s = 0; s < DEPTH; s++) issue_x(0, s, ring[s]);
     issue_w(0, 0);
     issue_w(1, 1);
     load_scales(0);
@@ -197,14 +203,15 @@ __global__ void __launch_bounds__(MXT_THREADS, 2) mx_tile_kernel(MxMat W, MxMat 
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __builtin_amdgcn_s_barrier();
     operands(0, 0, s0, 0);
-    for (int u0 = 0; u0 < units; u0 += 2) {
+    for (int u0 = 0; u0 < units; u0 += DEPTH / 2) {
         load_scales(u0 + 2);
 #pragma unroll
-        for (int s = 0; s < 2 * SPU; s += 4) {
-            stage(u0, s, s0, s1);
-            stage(u0, s + 1, s1, s2);
-            stage(u0, s + 2, s2, s3);
-            stage(u0, s + 3, s3, s0);
+        for (int s = 0; s < 2 * SPU; s++) stage(u0, s, ring[s % DEPTH], ring[(s + 1) % DEPTH]);
+        if constexpr (DEPTH == 8) {
+            // two more units: 2 SPU is 4 modulo 8
+            load_scales(u0 + 4);
+#pragma unroll
+            for (int s = 0; s < 2 * SPU; s++) stage(u0 + 2, s, ring[(s + 4) % 8], ring[(s + 5) % 8]);
         }
     }
     // no load may still be writing LDS when the block ends
