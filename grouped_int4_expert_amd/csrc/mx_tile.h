@@ -8,8 +8,8 @@
 // consecutive outputs of one row of y and stores them at once.
 //
 // One stage holds 128 bytes of each x row of the tile (64 bf16 inputs, or 256
-// MXFP4 inputs): loads write LDS directly, 16 bytes a lane, into a ring of
-// four stages.  Weights go to registers: a lane holds whole blocks of its
+// MXFP4 inputs): loads write LDS directly, 16 bytes a lane, into a ring of four
+// or eight stages.  Weights go to registers: a lane holds whole blocks of its
 // weight row, so one 16-byte load feeds 32 inputs and LDS carries x only.
 #pragma once
 

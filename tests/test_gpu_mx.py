@@ -608,3 +608,41 @@ def test_nonfinite_rows_in_tiles(kind):
     keep[rows] = False
     assert torch.equal(a[keep], b[keep])
     assert not torch.isfinite(b[rows]).any()
+
+
+# Calls that fill the GPU several times over, for the larger tiles: 64 and 128 rows of f32 and bf16, 128 and
+# 256 of MXFP4.
+@pytest.mark.parametrize("batch,rows,cols", [(1100, 4000, 1030), (2300, 4000, 1030), (4200, 4001, 1025)])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_large_tiles(kind, out, batch, rows, cols):
+    test_matmul(kind, out, batch, rows, cols)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_large_tiles(kind, gather):
+    say(f"mx grouped large tiles {kind} gather={gather}")
+    g = gen(31 + gather)
+    E, O, K = 9, 4000, 1030
+    off = torch.tensor([0, 700, 1, 0, 255, 1023, 640, 257, 129, 995]).cumsum(0).to(torch.int32)
+    n = int(off[-1])
+    q, s = ref.rand_mx(g, (E, O), K)
+    x, x_s, xv = rows_of(kind, g, n // 2 if gather else n, K)
+    pairs = torch.randint(0, n // 2 * 2, (n + 2,), generator=g).to(torch.int32) if gather else None
+    y = torch.full((n + 2 if gather else n, O), 3.0, device=DEV)
+    qm.qmoe_mx_grouped(qm.MxMat(q.to(DEV), s.to(DEV), K), x, off.to(DEV),
+                       pairs=None if pairs is None else pairs.to(DEV), k=2 if gather else 1, x_s=x_s, out=y)
+    src = pairs.numpy()[:n] // 2 if gather else np.arange(n)
+    want, m = np.zeros((n, O)), np.zeros((n, O))
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        want[a:b], m[a:b] = ref.product(ref.decode(q[e], s[e], K), xv[src[a:b]])
+    check(y[:n], want, ref.sum_bound(K, parts(kind)) * m, torch.float32, "grouped large tiles")
+    assert (y[n:] == 3.0).all()
+
+
+@pytest.mark.parametrize("T,E,H,F,k", [(700, 6, 1030, 1100, 4), (2000, 6, 1030, 1100, 4)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_layer_large_tiles(kind, T, E, H, F, k):
+    test_layer(kind, T, E, H, F, k)
